@@ -12,46 +12,14 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_checks.h"
 #include "kda_internal.h"
 
 namespace {
 
+using namespace kda::checks;
+
 thread_local char g_err[512] = "";
-
-kda_status fail(kda_status st, const char *fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof(g_err), fmt, ap);
-    va_end(ap);
-    return st;
-}
-
-kda_status hip_fail(hipError_t e, const char *what) {
-    return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-size_t esize(kda_dtype d) { return d == KDA_BF16 ? 2 : 4; }
-size_t state_esize(uint32_t flags) { return (flags & KDA_F_STATE_BF16) ? 2 : 4; }
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
-    return pa < pb + nb && pb < pa + na;
-}
-
-// Checks an optional host copy of cu_seqlens.
-kda_status check_cu_host(const int32_t *cu, int32_t n, int64_t total) {
-    if (!cu) return KDA_OK;
-    if (cu[0] != 0) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens[0] = %d, expected 0", cu[0]);
-    for (int32_t i = 0; i < n; ++i)
-        if (cu[i + 1] < cu[i])
-            return fail(KDA_ERR_INVALID_ARG, "cu_seqlens not monotone at %d (%d > %d)", i, cu[i],
-                        cu[i + 1]);
-    if ((int64_t)cu[n] != total)
-        return fail(KDA_ERR_INVALID_ARG, "cu_seqlens[%d] = %d, expected total_tokens = %lld", n,
-                    cu[n], (long long)total);
-    return KDA_OK;
-}
 
 kda_status check_common(int32_t num_seqs, int32_t H, int32_t dk, int32_t dv, kda_dtype dt,
                         uint32_t flags, float scale, float lb, uint32_t allowed = KDA_F_ALL) {
@@ -67,37 +35,6 @@ kda_status check_common(int32_t num_seqs, int32_t H, int32_t dk, int32_t dv, kda
         return fail(KDA_ERR_INVALID_ARG, "gate_lower_bound must be finite and < 0");
     if ((int64_t)num_seqs * H > (int64_t)1 << 26)
         return fail(KDA_ERR_INVALID_ARG, "num_seqs * num_heads too large");
-    return KDA_OK;
-}
-
-// Rows of the state and conv-state arrays: the pool size with a slot map, else
-// one per sequence.
-kda_status pool_rows(const int32_t *slots, int32_t num_slots, int32_t num_seqs, size_t &rows) {
-    if (!slots) {
-        rows = (size_t)num_seqs;
-        return KDA_OK;
-    }
-    if (num_slots < 1) return fail(KDA_ERR_INVALID_ARG, "state_slots needs num_slots >= 1");
-    rows = (size_t)num_slots;
-    return KDA_OK;
-}
-
-// A call's buffers as (pointer, bytes, name); the first `n_written` are written
-// by the call.  Every written buffer must overlap no other buffer of the call.
-// NULL or empty buffers overlap nothing; an allowed in-place pair is passed with
-// the input side's size set to 0.
-struct Buf {
-    const void *p;
-    size_t bytes;
-    const char *name;
-};
-kda_status check_written(const Buf *b, int n, int n_written) {
-    for (int i = 0; i < n_written; ++i)
-        for (int j = 0; j < n; ++j) {
-            if (j == i || (j < n_written && j < i)) continue;
-            if (overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
-                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
-        }
     return KDA_OK;
 }
 
@@ -182,6 +119,20 @@ void trace(const char *fmt, ...) {
     va_end(ap);
     std::fprintf(stderr, "[kda] %s\n", line);
 }
+
+namespace checks {
+
+kda_status fail(kda_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+void clear_error() { g_err[0] = 0; }
+
+}  // namespace checks
 
 constexpr int kDefaultSpinLimit = 1 << 22;
 std::atomic<int> g_spin_limit{kDefaultSpinLimit};

@@ -63,4 +63,12 @@ hipError_t launch_prefill_split(const kda_prefill_args *a, int dv_tile, const Sp
 // Fused schedule: one workgroup per (sequence, head), no workspace.
 hipError_t launch_prefill_fused(const kda_prefill_args *a, hipStream_t s);
 
+// Linear attention with one decay per head; strides and scale are resolved.
+hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t s);
+hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s);
+
+// Per-head norms: queries and keys with their rotation, and the gated output norm.
+hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t s);
+hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t s);
+
 }  // namespace kda

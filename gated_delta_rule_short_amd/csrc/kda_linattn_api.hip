@@ -1,0 +1,293 @@
+// kda_linattn_api.hip -- the extern "C" entry points of the linear attention and
+// the per-head norms (declared in kda.h).
+//
+// Every argument is checked on the host before anything is enqueued, as in
+// kda_api.hip; the library allocates nothing and never synchronises the stream.
+#include <algorithm>
+#include <cmath>
+
+#include "kda.h"
+#include "kda_checks.h"
+#include "kda_internal.h"
+
+namespace {
+
+using namespace kda::checks;
+
+// A [tokens][width] tensor with `stride` elements from one token to the next.
+struct Rows {
+    const void *p;
+    int64_t tokens, stride, width;
+    size_t elem;
+    const char *name;
+};
+
+size_t rows_bytes(const Rows &r) {
+    return r.p && r.tokens > 0 ? ((size_t)(r.tokens - 1) * (size_t)r.stride + (size_t)r.width) * r.elem : 0;
+}
+
+// Tensors of one stride that interleave without sharing an element (views of one
+// packed projection) do not overlap; any other pair is judged by its byte range.
+bool rows_overlap(const Rows &a, const Rows &b) {
+    if (!overlap(a.p, rows_bytes(a), b.p, rows_bytes(b))) return false;
+    const int64_t sa = a.stride * (int64_t)a.elem, sb = b.stride * (int64_t)b.elem;
+    if (sa != sb) return true;
+    int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % sa;
+    if (d < 0) d += sa;
+    return !(d >= a.width * (int64_t)a.elem && sa - d >= b.width * (int64_t)b.elem);
+}
+
+// Resolves a dense stride and checks what the kernels' 16-byte accesses need.
+kda_status check_rows(Rows &r) {
+    if (r.stride == 0) r.stride = r.width;
+    if (r.stride < r.width)
+        return fail(KDA_ERR_INVALID_ARG, "%s_stride = %lld, a token has %lld elements", r.name, (long long)r.stride,
+                    (long long)r.width);
+    if (r.stride > ((int64_t)1 << 40) / std::max<int64_t>(r.tokens, 1))
+        return fail(KDA_ERR_INVALID_ARG, "%s_stride = %lld is too large", r.name, (long long)r.stride);
+    if ((uintptr_t)r.p % 16 || (size_t)r.stride * r.elem % 16)
+        return fail(KDA_ERR_INVALID_ARG, "%s and its token stride must be 16-byte aligned", r.name);
+    return KDA_OK;
+}
+
+// The written tensors (the first n_written) against every other; `same` gives the
+// input a written tensor may be (equal pointer and stride), or -1.
+kda_status check_rows_written(const Rows *r, int n, int n_written, const int *same) {
+    for (int i = 0; i < n_written; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (j == i || (j < n_written && j < i)) continue;
+            if (j >= n_written && same[i] == j && r[i].p == r[j].p && r[i].stride == r[j].stride) continue;
+            if (rows_overlap(r[i], r[j]))
+                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", r[i].name, r[j].name);
+        }
+    return KDA_OK;
+}
+
+kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv, kda_dtype dt, uint32_t flags,
+                         float scale) {
+    if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs = %d, must be >= 1", N);
+    if (H < 1) return fail(KDA_ERR_INVALID_ARG, "num_heads = %d, must be >= 1", H);
+    if (Hk < 1 || H % Hk)
+        return fail(KDA_ERR_INVALID_ARG, "num_k_heads = %d, must divide num_heads = %d", Hk, H);
+    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128))
+        return fail(KDA_ERR_UNSUPPORTED, "head dims %d x %d: 64 and 128 are supported", dk, dv);
+    if (dt != KDA_F32 && dt != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (flags & ~(uint32_t)(KDA_F_STATE_BF16 | KDA_F_DECAY_PER_HEAD))
+        return fail(KDA_ERR_UNSUPPORTED, "unsupported flags 0x%x", flags);
+    if (!std::isfinite(scale) || scale < 0.f)
+        return fail(KDA_ERR_INVALID_ARG, "scale must be finite and >= 0 (0 = default)");
+    // a launch holds fewer than 2^32 threads, up to 1024 of them for each pair
+    if ((int64_t)N * H >= (int64_t)1 << 22)
+        return fail(KDA_ERR_INVALID_ARG, "num_seqs * num_heads too large");
+    return KDA_OK;
+}
+
+kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) {
+    kda_status st = check_linattn(a.num_seqs, a.num_heads, a.num_k_heads, a.head_dim_k, a.head_dim_v, a.dtype,
+                                  a.flags, a.scale);
+    if (st != KDA_OK) return st;
+    const int64_t T = a.total_tokens, H = a.num_heads, N = a.num_seqs;
+    if (T < 0) return fail(KDA_ERR_INVALID_ARG, "total_tokens < 0");
+    // token positions inside a sequence are 32-bit in the kernels (cu_seqlens is int32)
+    if (T > ((int64_t)1 << 31) - 64) return fail(KDA_ERR_INVALID_ARG, "total_tokens too large");
+    if (T > 0 && (!a.q || !a.k || !a.v || !a.o))
+        return fail(KDA_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
+    if (T > 0 && !a.log_decay) return fail(KDA_ERR_INVALID_ARG, "log_decay is NULL");
+    if (a.cu_seqlens_host && !a.cu_seqlens)
+        return fail(KDA_ERR_INVALID_ARG, "cu_seqlens_host needs cu_seqlens");
+    if (!a.cu_seqlens && T % N)
+        return fail(KDA_ERR_INVALID_ARG, "cu_seqlens NULL needs total_tokens %% num_seqs == 0");
+    st = check_cu_host(a.cu_seqlens_host, a.num_seqs, T);
+    if (st != KDA_OK) return st;
+    const size_t es = esize(a.dtype);
+    size_t rows = 0;
+    st = pool_rows(a.state_slots, a.num_slots, a.num_seqs, rows);
+    if (st != KDA_OK) return st;
+    const size_t sb = rows * H * a.head_dim_k * a.head_dim_v * state_esize(a.flags);
+    const int64_t wk = (int64_t)a.num_k_heads * a.head_dim_k, wv = H * a.head_dim_v;
+    Rows r[4] = {{a.o, T, wv, wv, es, "o"}, {a.q, T, a.q_stride, wk, es, "q"}, {a.k, T, a.k_stride, wk, es, "k"},
+                 {a.v, T, a.v_stride, wv, es, "v"}};
+    for (Rows &x : r) {
+        st = check_rows(x);
+        if (st != KDA_OK) return st;
+    }
+    a.q_stride = r[1].stride; a.k_stride = r[2].stride; a.v_stride = r[3].stride;
+    if ((uintptr_t)a.state_in % 16 || (uintptr_t)a.state_out % 16)
+        return fail(KDA_ERR_INVALID_ARG, "the states must be 16-byte aligned");
+    const bool in_place = a.state_out && (const void *)a.state_out == a.state_in;
+    if (a.state_out && !in_place && overlap(a.state_out, sb, a.state_in, sb))
+        return fail(KDA_ERR_INVALID_ARG, "state_out partially overlaps state_in");
+    const size_t gb = (size_t)H * ((a.flags & KDA_F_DECAY_PER_HEAD) ? 1 : T) * 4;
+    const Buf bufs[] = {{a.o, rows_bytes(r[0]), "o"}, {a.state_out, sb, "state_out"},
+                        {a.q, rows_bytes(r[1]), "q"}, {a.k, rows_bytes(r[2]), "k"}, {a.v, rows_bytes(r[3]), "v"},
+                        {a.log_decay, gb, "log_decay"}, {a.state_in, in_place ? 0 : sb, "state_in"},
+                        {a.cu_seqlens, a.cu_seqlens ? (size_t)(N + 1) * 4 : 0, "cu_seqlens"},
+                        {a.state_slots, a.state_slots ? (size_t)N * 4 : 0, "state_slots"}};
+    st = check_written(bufs, 9, 2);
+    if (st != KDA_OK) return st;
+    if (T == 0 && !a.state_out) return KDA_OK;
+    if (a.scale == 0.f) a.scale = 1.0f / std::sqrt((float)a.head_dim_k);
+    hipError_t e = kda::launch_linattn_prefill(&a, stream);
+    if (e != hipSuccess) return hip_fail(e, "linattn_prefill launch");
+    return KDA_OK;
+}
+
+kda_status linattn_decode_impl(kda_linattn_decode_args a, hipStream_t stream) {
+    kda_status st = check_linattn(a.num_seqs, a.num_heads, a.num_k_heads, a.head_dim_k, a.head_dim_v, a.dtype,
+                                  a.flags, a.scale);
+    if (st != KDA_OK) return st;
+    if (!a.q || !a.k || !a.v || !a.log_decay || !a.state || !a.o)
+        return fail(KDA_ERR_INVALID_ARG, "q, k, v, log_decay, state and o must be non-NULL");
+    const size_t es = esize(a.dtype);
+    const int64_t N = a.num_seqs, H = a.num_heads;
+    size_t rows = 0;
+    st = pool_rows(a.state_slots, a.num_slots, a.num_seqs, rows);
+    if (st != KDA_OK) return st;
+    const size_t sb = rows * H * a.head_dim_k * a.head_dim_v * state_esize(a.flags);
+    const int64_t wk = (int64_t)a.num_k_heads * a.head_dim_k, wv = H * a.head_dim_v;
+    Rows r[4] = {{a.o, N, wv, wv, es, "o"}, {a.q, N, a.q_stride, wk, es, "q"}, {a.k, N, a.k_stride, wk, es, "k"},
+                 {a.v, N, a.v_stride, wv, es, "v"}};
+    for (Rows &x : r) {
+        st = check_rows(x);
+        if (st != KDA_OK) return st;
+    }
+    a.q_stride = r[1].stride; a.k_stride = r[2].stride; a.v_stride = r[3].stride;
+    if ((uintptr_t)a.state % 16) return fail(KDA_ERR_INVALID_ARG, "the states must be 16-byte aligned");
+    const Buf bufs[] = {{a.o, rows_bytes(r[0]), "o"}, {a.state, sb, "state"},
+                        {a.q, rows_bytes(r[1]), "q"}, {a.k, rows_bytes(r[2]), "k"}, {a.v, rows_bytes(r[3]), "v"},
+                        {a.log_decay, (size_t)H * ((a.flags & KDA_F_DECAY_PER_HEAD) ? 1 : N) * 4, "log_decay"},
+                        {a.state_slots, a.state_slots ? (size_t)N * 4 : 0, "state_slots"}};
+    st = check_written(bufs, 7, 2);
+    if (st != KDA_OK) return st;
+    if (a.scale == 0.f) a.scale = 1.0f / std::sqrt((float)a.head_dim_k);
+    hipError_t e = kda::launch_linattn_decode(&a, stream);
+    if (e != hipSuccess) return hip_fail(e, "linattn_decode launch");
+    return KDA_OK;
+}
+
+// Checks shared by the two norms.
+kda_status check_norm(int64_t T, int32_t D, kda_dtype dt, float eps) {
+    if (T < 0) return fail(KDA_ERR_INVALID_ARG, "total_tokens < 0");
+    if (T > ((int64_t)1 << 31) - 64) return fail(KDA_ERR_INVALID_ARG, "total_tokens too large");
+    if (D != 64 && D != 128) return fail(KDA_ERR_UNSUPPORTED, "head_dim %d: 64 and 128 are supported", D);
+    if (dt != KDA_F32 && dt != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (!std::isfinite(eps) || !(eps > 0.f)) return fail(KDA_ERR_INVALID_ARG, "eps must be finite and > 0");
+    return KDA_OK;
+}
+
+kda_status qk_norm_rope_impl(kda_qk_norm_rope_args a, hipStream_t stream) {
+    kda_status st = check_norm(a.total_tokens, a.head_dim, a.dtype, a.eps);
+    if (st != KDA_OK) return st;
+    const int64_t T = a.total_tokens;
+    const int32_t D = a.head_dim, R = a.rotary_dim;
+    if (a.num_q_heads < 1 || a.num_q_heads > 1 << 16)
+        return fail(KDA_ERR_INVALID_ARG, "num_q_heads = %d, must be in 1..65536", a.num_q_heads);
+    if (a.num_k_heads < 0 || a.num_k_heads > 1 << 16)
+        return fail(KDA_ERR_INVALID_ARG, "num_k_heads = %d, must be in 0..65536", a.num_k_heads);
+    if (a.norm != KDA_NORM_NONE && a.norm != KDA_NORM_RMS && a.norm != KDA_NORM_L2)
+        return fail(KDA_ERR_INVALID_ARG, "norm %d: use a KDA_NORM_* value", (int)a.norm);
+    if (a.flags & ~(uint32_t)KDA_F_ROPE_INTERLEAVED)
+        return fail(KDA_ERR_UNSUPPORTED, "unsupported flags 0x%x", a.flags);
+    if (R < 0 || R > D || R % 16)
+        return fail(KDA_ERR_UNSUPPORTED, "rotary_dim %d: a multiple of 16 up to head_dim = %d", R, D);
+    if (a.norm != KDA_NORM_RMS && (a.q_weight || a.k_weight))
+        return fail(KDA_ERR_INVALID_ARG, "weights need KDA_NORM_RMS");
+    if (T == 0) return KDA_OK;  // empty tensors may be NULL
+    if ((R == 0) != !a.positions || (R == 0) != !a.inv_freq)
+        return fail(KDA_ERR_INVALID_ARG, "positions and inv_freq go with rotary_dim > 0, and only with it");
+    if (a.num_k_heads == 0 && (a.k || a.k_out || a.k_weight))
+        return fail(KDA_ERR_INVALID_ARG, "num_k_heads = 0 takes no k, k_out or k_weight");
+    if (!a.q || !a.q_out || (a.num_k_heads > 0 && (!a.k || !a.k_out)))
+        return fail(KDA_ERR_INVALID_ARG, "q, q_out, k and k_out must be non-NULL");
+    const size_t es = esize(a.dtype);
+    const int64_t wq = (int64_t)a.num_q_heads * D, wk = (int64_t)a.num_k_heads * D;
+    Rows r[4] = {{a.q_out, T, a.q_out_stride, wq, es, "q_out"}, {a.k_out, T, a.k_out_stride, wk, es, "k_out"},
+                 {a.q, T, a.q_stride, wq, es, "q"}, {a.k, T, a.k_stride, wk, es, "k"}};
+    for (Rows &x : r) {
+        st = check_rows(x);
+        if (st != KDA_OK) return st;
+    }
+    a.q_out_stride = r[0].stride; a.k_out_stride = r[1].stride;
+    a.q_stride = r[2].stride; a.k_stride = r[3].stride;
+    const int same[2] = {2, 3};
+    st = check_rows_written(r, 4, 2, same);
+    if (st != KDA_OK) return st;
+    if ((uintptr_t)a.q_weight % 16 || (uintptr_t)a.k_weight % 16)
+        return fail(KDA_ERR_INVALID_ARG, "the weights must be 16-byte aligned");
+    const Buf aux[] = {{a.q_out, rows_bytes(r[0]), "q_out"}, {a.k_out, rows_bytes(r[1]), "k_out"},
+                       {a.q_weight, a.q_weight ? (size_t)D * 4 : 0, "q_weight"},
+                       {a.k_weight, a.k_weight ? (size_t)D * 4 : 0, "k_weight"},
+                       {a.positions, a.positions ? (size_t)T * 4 : 0, "positions"},
+                       {a.inv_freq, (size_t)R * 2, "inv_freq"}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 2; j < 6; ++j)
+            if (overlap(aux[i].p, aux[i].bytes, aux[j].p, aux[j].bytes))
+                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", aux[i].name, aux[j].name);
+    hipError_t e = kda::launch_qk_norm_rope(&a, stream);
+    if (e != hipSuccess) return hip_fail(e, "qk_norm_rope launch");
+    return KDA_OK;
+}
+
+kda_status gated_norm_impl(kda_gated_norm_args a, hipStream_t stream) {
+    kda_status st = check_norm(a.total_tokens, a.head_dim, a.dtype, a.eps);
+    if (st != KDA_OK) return st;
+    const int64_t T = a.total_tokens;
+    if (a.num_heads < 1 || a.num_heads > 1 << 16)
+        return fail(KDA_ERR_INVALID_ARG, "num_heads = %d, must be in 1..65536", a.num_heads);
+    if (a.flags & ~(uint32_t)(KDA_F_SILU | KDA_F_WEIGHT_PER_HEAD))
+        return fail(KDA_ERR_UNSUPPORTED, "unsupported flags 0x%x", a.flags);
+    if (T == 0) return KDA_OK;  // empty tensors may be NULL
+    if ((a.flags & KDA_F_WEIGHT_PER_HEAD) && !a.weight)
+        return fail(KDA_ERR_INVALID_ARG, "KDA_F_WEIGHT_PER_HEAD needs a weight");
+    if ((a.flags & KDA_F_SILU) && !a.z) return fail(KDA_ERR_INVALID_ARG, "KDA_F_SILU needs z");
+    if (!a.x || !a.y) return fail(KDA_ERR_INVALID_ARG, "x and y must be non-NULL");
+    const size_t es = esize(a.dtype);
+    const int64_t w = (int64_t)a.num_heads * a.head_dim;
+    Rows r[3] = {{a.y, T, a.y_stride, w, es, "y"}, {a.x, T, a.x_stride, w, es, "x"},
+                 {a.z, T, a.z ? a.z_stride : 0, w, es, "z"}};
+    for (Rows &x : r) {
+        st = check_rows(x);
+        if (st != KDA_OK) return st;
+    }
+    a.y_stride = r[0].stride; a.x_stride = r[1].stride; a.z_stride = r[2].stride;
+    for (int j = 1; j < 3; ++j) {  // y may be x or z, element for element
+        if (r[0].p == r[j].p && r[0].stride == r[j].stride) continue;
+        if (rows_overlap(r[0], r[j])) return fail(KDA_ERR_INVALID_ARG, "y overlaps %s", r[j].name);
+    }
+    if ((uintptr_t)a.weight % 16) return fail(KDA_ERR_INVALID_ARG, "the weight must be 16-byte aligned");
+    const size_t wb = !a.weight ? 0 : (size_t)a.head_dim * ((a.flags & KDA_F_WEIGHT_PER_HEAD) ? a.num_heads : 1) * 4;
+    if (overlap(a.y, rows_bytes(r[0]), a.weight, wb)) return fail(KDA_ERR_INVALID_ARG, "y overlaps weight");
+    hipError_t e = kda::launch_gated_norm(&a, stream);
+    if (e != hipSuccess) return hip_fail(e, "gated_norm launch");
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t stream) {
+    clear_error();
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    return linattn_prefill_impl(*a, stream);
+}
+
+kda_status kda_linattn_decode(const kda_linattn_decode_args *a, hipStream_t stream) {
+    clear_error();
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    return linattn_decode_impl(*a, stream);
+}
+
+kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t stream) {
+    clear_error();
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    return qk_norm_rope_impl(*a, stream);
+}
+
+kda_status kda_gated_norm(const kda_gated_norm_args *a, hipStream_t stream) {
+    clear_error();
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    return gated_norm_impl(*a, stream);
+}
+
+}  // extern "C"

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libkda.so")
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_HIP = 0, 1, 2, 3
 KDA_F32, KDA_BF16 = 0, 1
 KDA_F_SILU, KDA_F_NO_QK_L2NORM, KDA_F_GATE_IS_LOG, KDA_F_STATE_BF16 = 1, 2, 4, 8
+KDA_F_DECAY_PER_HEAD, KDA_F_ROPE_INTERLEAVED, KDA_F_WEIGHT_PER_HEAD = 256, 512, 1024
+NORMS = {"none": 0, "rms": 1, "l2": 2}  # kda_norm
 PREFILL_WORKSPACE_CAP = 4 << 30  # KDA_PREFILL_WORKSPACE_CAP
 PREFILL_SCRATCH_BYTES = 256 << 20  # KDA_PREFILL_SCRATCH_BYTES (kda_prefill_noalloc)
 
@@ -26,7 +28,8 @@ EXPORTS = ("kda_abi_version", "kda_set_spin_limit", "kda_status_string", "kda_la
            "kda_prefill", "kda_prefill_workspace_size", "kda_prefill_workspace_full_size",
            "kda_prefill_workspace_min_size", "kda_prefill_noalloc", "kda_decode", "kda_decode_multi",
            "kda_decode_commit", "kda_state_copy", "kda_gate_beta_proj",
-           "kda_gate_beta_workspace_size")
+           "kda_gate_beta_workspace_size", "kda_linattn_prefill", "kda_linattn_decode",
+           "kda_qk_norm_rope", "kda_gated_norm")
 MAX_SPEC_TOKENS = 8
 UPDATE_FLOATS = 6 * 128  # floats per (sequence, head, token) update record
 
@@ -112,6 +115,49 @@ class KdaGateBetaArgs(ctypes.Structure):
     ]
 
 
+class KdaLinattnPrefillArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", _c_i32), ("num_heads", _c_i32), ("num_k_heads", _c_i32),
+        ("head_dim_k", _c_i32), ("head_dim_v", _c_i32), ("dtype", ctypes.c_int),
+        ("total_tokens", _c_i64), ("q_stride", _c_i64), ("k_stride", _c_i64), ("v_stride", _c_i64),
+        ("flags", _c_u32), ("scale", _c_f32),
+        ("q", _p), ("k", _p), ("v", _p), ("log_decay", _p), ("state_in", _p), ("state_out", _p),
+        ("o", _p), ("cu_seqlens", _p), ("cu_seqlens_host", _p), ("state_slots", _p),
+        ("num_slots", _c_i32),
+    ]
+
+
+class KdaLinattnDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", _c_i32), ("num_heads", _c_i32), ("num_k_heads", _c_i32),
+        ("head_dim_k", _c_i32), ("head_dim_v", _c_i32), ("dtype", ctypes.c_int),
+        ("q_stride", _c_i64), ("k_stride", _c_i64), ("v_stride", _c_i64),
+        ("flags", _c_u32), ("scale", _c_f32),
+        ("q", _p), ("k", _p), ("v", _p), ("log_decay", _p), ("state", _p), ("o", _p),
+        ("state_slots", _p), ("num_slots", _c_i32),
+    ]
+
+
+class KdaQkNormRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _c_i64), ("num_q_heads", _c_i32), ("num_k_heads", _c_i32),
+        ("head_dim", _c_i32), ("rotary_dim", _c_i32), ("dtype", ctypes.c_int), ("norm", ctypes.c_int),
+        ("flags", _c_u32), ("eps", _c_f32),
+        ("q_stride", _c_i64), ("k_stride", _c_i64), ("q_out_stride", _c_i64), ("k_out_stride", _c_i64),
+        ("q", _p), ("k", _p), ("q_out", _p), ("k_out", _p), ("q_weight", _p), ("k_weight", _p),
+        ("positions", _p), ("inv_freq", _p),
+    ]
+
+
+class KdaGatedNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _c_i64), ("num_heads", _c_i32), ("head_dim", _c_i32), ("dtype", ctypes.c_int),
+        ("flags", _c_u32), ("eps", _c_f32),
+        ("x_stride", _c_i64), ("z_stride", _c_i64), ("y_stride", _c_i64),
+        ("x", _p), ("z", _p), ("weight", _p), ("y", _p),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__("%s: %s" % (status, msg))
@@ -160,6 +206,11 @@ def load_library(path: str = LIB_PATH):
         lib.kda_gate_beta_workspace_size.argtypes = [ctypes.POINTER(KdaGateBetaArgs)]
         lib.kda_state_copy.restype = ctypes.c_int
         lib.kda_state_copy.argtypes = [ctypes.POINTER(KdaStateCopyArgs), _p]
+        for f, args in (("kda_linattn_prefill", KdaLinattnPrefillArgs),
+                        ("kda_linattn_decode", KdaLinattnDecodeArgs),
+                        ("kda_qk_norm_rope", KdaQkNormRopeArgs), ("kda_gated_norm", KdaGatedNormArgs)):
+            getattr(lib, f).restype = ctypes.c_int
+            getattr(lib, f).argtypes = [ctypes.POINTER(args), _p]
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -172,6 +223,10 @@ def _check(lib, status):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_code(t):
@@ -654,6 +709,243 @@ def gate_beta_workspace_bytes(total_tokens, num_heads):
     lib = load_library()
     a = KdaGateBetaArgs(total_tokens=int(total_tokens), num_heads=int(num_heads))
     return int(lib.kda_gate_beta_workspace_size(ctypes.byref(a)))
+
+
+# ------------------------------------------------------------------ linear attention, per-head norms
+def _rows(t, name, T, heads, d, dtype, dev):
+    """Token stride of a [T, heads, d] tensor whose heads are dense (0: dense tokens too)."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError("%s must have shape %s, got %s" % (name, (T, heads, d), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+    st, sh, sd = t.stride()
+    if T == 0:
+        return 0
+    if sd != 1 or (heads > 1 and sh != d):
+        raise ValueError("the heads of %s must be dense: strides %s" % (name, t.stride()))
+    if T == 1:
+        return 0
+    if st < heads * d:
+        raise ValueError("the tokens of %s must not overlap: strides %s" % (name, t.stride()))
+    return st
+
+
+class _on:
+    """The device (and stream) a call runs on: its allocations and launches belong
+    there, whichever device and stream the caller's thread is on."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a GPU, got %s" % (dev,))
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _decay(log_decay, T, H, dev):
+    """KDA_F_DECAY_PER_HEAD for an [H] log-decay, 0 for [T, H]."""
+    _need(log_decay, "log_decay", torch.float32, dev)
+    if log_decay.dim() == 1:
+        _shape(log_decay, "log_decay", (H,))
+        return KDA_F_DECAY_PER_HEAD
+    _shape(log_decay, "log_decay", (T, H))
+    return 0
+
+
+def _linattn_shapes(q, v):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [T, Hk, dk] and v [T, H, dv], got %s and %s" % (tuple(q.shape), tuple(v.shape)))
+    return q.shape + v.shape[1:]
+
+
+def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=None, num_seqs=None,
+                        state_in=None, state_out=None, o=None, scale=0.0, state_slots=None, stream=None):
+    """Linear attention with one decay per head over packed sequences (kda_linattn_prefill):
+    S <- exp(g) S + k v^T, o = scale S^T q per token.
+
+    q, k: [T, Hk, dk], v: [T, H, dv] (bf16 or fp32, one dtype; heads dense, tokens at any
+    stride of whole 16 bytes, as in views of a packed projection); head h reads key head
+    h // (H // Hk); dk and dv are 64 or 128.  log_decay: fp32, [T, H], or [H] for every
+    token.  The state is [N, H, dk, dv] fp32, or bf16 storage when those tensors are bf16;
+    with state_slots (int32 [N]) the state tensors are pools and sequence n uses row
+    state_slots[n].  state_out: a tensor, or True to allocate one of state_in's dtype
+    (else fp32).  scale 0 is 1 / sqrt(dk).  Returns (o [T, H, dv], state_out)."""
+    lib = load_library()
+    dev, dt = q.device, q.dtype
+    T, Hk, dk, H, dv = _linattn_shapes(q, v)
+    N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else int(num_seqs or 1)
+    qs, ks, vs = (_rows(q, "q", T, Hk, dk, dt, dev), _rows(k, "k", T, Hk, dk, dt, dev),
+                  _rows(v, "v", T, H, dv, dt, dev))
+    flags = _decay(log_decay, T, H, dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        _shape(cu_seqlens, "cu_seqlens", (N + 1,))
+    cuh = None
+    if cu_seqlens_host is not None:
+        cuh = torch.as_tensor(cu_seqlens_host, dtype=torch.int32, device="cpu").contiguous()
+        _shape(cuh, "cu_seqlens_host", (N + 1,))
+    if state_slots is not None and not torch.is_tensor(state_out) and (state_out or state_in is None):
+        raise ValueError("with state_slots, pass the pool tensors as state_in / state_out")
+    sdt = state_in.dtype if state_in is not None else state_out.dtype if torch.is_tensor(state_out) else torch.float32
+    for t, nm in ((state_in, "state_in"), (state_out, "state_out")):
+        if torch.is_tensor(t):
+            _need(t, nm, None, dev)
+            _pool_shape(t, nm, (H, dk, dv))
+            if t.dtype != sdt:
+                raise TypeError("state_in and state_out must have one dtype")
+            flags |= _state_flag(t)
+    slots, num_slots = _slots(state_slots, (state_in, state_out), N, dev)
+    if o is not None:
+        _need(o, "o", dt, dev)
+        _shape(o, "o", (T, H, dv))
+    code = _dtype_code(q)
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty((T, H, dv), dtype=dt, device=dev)
+        if state_out is True:
+            state_out = torch.empty((N, H, dk, dv), dtype=sdt, device=dev)
+        elif state_out is False:
+            state_out = None
+        a = KdaLinattnPrefillArgs(
+            N, H, Hk, dk, dv, code, T, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            log_decay.data_ptr(), _addr(state_in), _addr(state_out), o.data_ptr(), _addr(cu_seqlens), _addr(cuh),
+            slots, num_slots)
+        _check(lib, lib.kda_linattn_prefill(ctypes.byref(a), _stream(stream, dev)))
+    return o, state_out
+
+
+def kda_linattn_decode(q, k, v, log_decay, state, *, o=None, scale=0.0, state_slots=None, stream=None):
+    """One token of linear attention with one decay per head for each of N sequences
+    (kda_linattn_decode): q, k [N, Hk, dk], v [N, H, dv], log_decay [N, H] or [H] fp32;
+    state [N, H, dk, dv] (fp32, or bf16 storage), or a pool with state_slots, is updated
+    in place.  Shapes, strides and types as in kda_linattn_prefill.  Returns o [N, H, dv]."""
+    lib = load_library()
+    dev, dt = q.device, q.dtype
+    N, Hk, dk, H, dv = _linattn_shapes(q, v)
+    qs, ks, vs = (_rows(q, "q", N, Hk, dk, dt, dev), _rows(k, "k", N, Hk, dk, dt, dev),
+                  _rows(v, "v", N, H, dv, dt, dev))
+    flags = _decay(log_decay, N, H, dev) | _state_flag(state)
+    _need(state, "state", None, dev)
+    _pool_shape(state, "state", (H, dk, dv))
+    slots, num_slots = _slots(state_slots, (state,), N, dev)
+    if o is not None:
+        _need(o, "o", dt, dev)
+        _shape(o, "o", (N, H, dv))
+    code = _dtype_code(q)
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty((N, H, dv), dtype=dt, device=dev)
+        a = KdaLinattnDecodeArgs(N, H, Hk, dk, dv, code, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), o.data_ptr(), slots,
+                                 num_slots)
+        _check(lib, lib.kda_linattn_decode(ctypes.byref(a), _stream(stream, dev)))
+    return o
+
+
+def kda_qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, positions=None,
+                     inv_freq=None, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of every head's query and key, then the rotation by position, in one pass
+    (kda_qk_norm_rope).  q [T, Hq, D], k [T, Hk, D] or None (bf16 or fp32, heads dense,
+    tokens at any stride of whole 16 bytes); D is 64 or 128.  norm: "rms" (q_weight and
+    k_weight [D] fp32, or None for ones), "l2" or "none".  positions int32 [T] and
+    inv_freq fp32 [R / 2] (R a multiple of 16) rotate the first R elements of each head,
+    in halves, or in adjacent pairs with interleaved=True; without them nothing is
+    rotated.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
+    lib = load_library()
+    dev, dt = q.device, q.dtype
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D], got %s" % (tuple(q.shape),))
+    T, Hq, D = q.shape
+    qs = _rows(q, "q", T, Hq, D, dt, dev)
+    Hk = ks = qos = kos = 0
+    if k is not None:
+        if k.dim() != 3 or k.shape[1] == 0:
+            raise ValueError("k must be [T, Hk, D], got %s" % (tuple(k.shape),))
+        Hk = k.shape[1]
+        ks = _rows(k, "k", T, Hk, D, dt, dev)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    if norm not in NORMS:
+        raise ValueError("norm must be one of %s" % sorted(NORMS))
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, nm, torch.float32, dev)
+            _shape(t, nm, (D,))
+    R = 0
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev)
+        _shape(positions, "positions", (T,))
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1 or inv_freq.numel() == 0:
+            raise ValueError("inv_freq must be [R / 2], got %s" % (tuple(inv_freq.shape),))
+        R = 2 * inv_freq.numel()
+    if q_out is not None:
+        qos = _rows(q_out, "q_out", T, Hq, D, dt, dev)
+    if k_out is not None:
+        kos = _rows(k_out, "k_out", T, Hk, D, dt, dev)
+    code = _dtype_code(q)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
+        a = KdaQkNormRopeArgs(T, Hq, Hk, D, R, code, NORMS[norm], KDA_F_ROPE_INTERLEAVED if interleaved else 0, eps,
+                              qs, ks, qos, kos, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
+                              _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq))
+        _check(lib, lib.kda_qk_norm_rope(ctypes.byref(a), _stream(stream, dev)))
+    return q_out, k_out
+
+
+def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, y=None, stream=None):
+    """RMS norm of every head of a mixer's output times an activated gate
+    (kda_gated_norm): y = weight * x / rms(x) * act(gate), act "sigmoid" or "silu".
+    x, gate, y: [T, H, D] (bf16 or fp32, heads dense, tokens at any stride of whole 16
+    bytes), D 64 or 128; gate None leaves the factor out; weight fp32 [D], [H, D] or
+    None.  y may be x or gate.  Returns y."""
+    lib = load_library()
+    dev, dt = x.device, x.dtype
+    if x.dim() != 3:
+        raise ValueError("x must be [T, H, D], got %s" % (tuple(x.shape),))
+    T, H, D = x.shape
+    xs = _rows(x, "x", T, H, D, dt, dev)
+    zs = ys = flags = 0
+    if act not in ("sigmoid", "silu"):
+        raise ValueError("act must be 'sigmoid' or 'silu'")
+    if gate is not None:
+        zs = _rows(gate, "gate", T, H, D, dt, dev)
+        flags |= KDA_F_SILU if act == "silu" else 0
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev)
+        if weight.dim() == 2:
+            _shape(weight, "weight", (H, D))
+            flags |= KDA_F_WEIGHT_PER_HEAD
+        else:
+            _shape(weight, "weight", (D,))
+    if y is not None:
+        ys = _rows(y, "y", T, H, D, dt, dev)
+    code = _dtype_code(x)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((T, H, D), dtype=dt, device=dev)
+        a = KdaGatedNormArgs(T, H, D, code, flags, eps, xs, zs, ys, x.data_ptr(), _addr(gate), _addr(weight),
+                             y.data_ptr())
+        _check(lib, lib.kda_gated_norm(ctypes.byref(a), _stream(stream, dev)))
+    return y
 
 
 # ------------------------------------------------------------------ calibration

@@ -481,6 +481,139 @@ kda_status kda_gate_beta_proj(const kda_gate_beta_args *args, hipStream_t stream
  * product's fp32 partials, then 2 T r for z. */
 size_t kda_gate_beta_workspace_size(const kda_gate_beta_args *args);
 
+/*
+ * Linear attention with one decay per head: the other recurrence that shares
+ * this library's state pool, beside the channel-wise gate and the delta rule
+ * above.  Per token t of a sequence and head h, with key head h / (H / Hk):
+ *     S   <- exp(min(g_t, 0)) S + k_t v_t^T
+ *     o_t =  scale * S^T q_t
+ * No conv, normalisation or activation is applied: q and k arrive as the
+ * recurrence uses them (kda_qk_norm_rope prepares them, kda_gated_norm takes o
+ * on to the output projection).
+ *
+ * Layouts: q, k [T][Hk][dk], v and o [T][H][dv], state [N][H][dk][dv], all with
+ * the last two indices dense.  q_stride, k_stride and v_stride give the elements
+ * from one token to the next (views of a packed projection), 0 meaning dense;
+ * o is dense.  The log-decay g is fp32, [T][H], or [H] for every token with
+ * KDA_F_DECAY_PER_HEAD; positive values count as 0 and -inf clears the state.
+ * dk and dv are 64 or 128.  Tensor bases, strides and states are 16-byte
+ * aligned.  state_slots works as in "State pool" above.
+ * A non-finite q, k, v or g reaches the outputs of its own and later tokens of
+ * its sequence and head, and no others.
+ */
+#define KDA_F_DECAY_PER_HEAD 256u
+
+typedef struct {
+    int32_t num_seqs;        /* N >= 1 */
+    int32_t num_heads;       /* H >= 1: heads of v, o, the decay and the state */
+    int32_t num_k_heads;     /* Hk >= 1, divides H: heads of q and k */
+    int32_t head_dim_k;      /* 64 or 128 */
+    int32_t head_dim_v;      /* 64 or 128 */
+    kda_dtype dtype;         /* of q, k, v and o */
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int64_t q_stride, k_stride, v_stride; /* elements per token, 0 = dense */
+    uint32_t flags;          /* KDA_F_STATE_BF16, KDA_F_DECAY_PER_HEAD */
+    float scale;             /* 0 = 1/sqrt(dk) */
+    const void *q, *k;       /* [T][Hk][dk] */
+    const void *v;           /* [T][H][dv] */
+    const float *log_decay;  /* [T][H], or [H] */
+    const void *state_in;    /* [N][H][dk][dv] fp32 (bf16 with KDA_F_STATE_BF16) or NULL (zeros) */
+    void *state_out;         /* same type, or NULL; may alias state_in */
+    void *o;                 /* [T][H][dv]; must not overlap the inputs */
+    const int32_t *cu_seqlens;      /* [N+1] device, or NULL for N equal sequences */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated when given */
+    const int32_t *state_slots;     /* [N] device pool slots, or NULL */
+    int32_t num_slots;              /* pool rows when state_slots is given */
+} kda_linattn_prefill_args;
+
+/* Packed prompts: every sequence from its initial state to its final one.
+ * Empty sequences pass their state through. */
+kda_status kda_linattn_prefill(const kda_linattn_prefill_args *args, hipStream_t stream);
+
+typedef struct {
+    int32_t num_seqs;        /* N >= 1: one token each */
+    int32_t num_heads;       /* H >= 1 */
+    int32_t num_k_heads;     /* Hk >= 1, divides H */
+    int32_t head_dim_k;      /* 64 or 128 */
+    int32_t head_dim_v;      /* 64 or 128 */
+    kda_dtype dtype;
+    int64_t q_stride, k_stride, v_stride; /* elements per sequence, 0 = dense */
+    uint32_t flags;          /* KDA_F_STATE_BF16, KDA_F_DECAY_PER_HEAD */
+    float scale;             /* 0 = 1/sqrt(dk) */
+    const void *q, *k;       /* [N][Hk][dk] */
+    const void *v;           /* [N][H][dv] */
+    const float *log_decay;  /* [N][H], or [H] */
+    void *state;             /* [N][H][dk][dv] in/out: the layout prefill writes */
+    void *o;                 /* [N][H][dv] */
+    const int32_t *state_slots;
+    int32_t num_slots;
+} kda_linattn_decode_args;
+
+/* One new token for each of N sequences, the states updated in place. */
+kda_status kda_linattn_decode(const kda_linattn_decode_args *args, hipStream_t stream);
+
+/*
+ * kda_qk_norm_rope -- every head's query and key normalised, then rotated by
+ * its position, in one pass over both tensors.  Per token and head, x of D
+ * elements:
+ *     y = w * x / sqrt(|x|^2 / D + eps)   KDA_NORM_RMS (w of D fp32, NULL = 1)
+ *     y = x / sqrt(|x|^2 + eps)           KDA_NORM_L2
+ *     y = x                               KDA_NORM_NONE
+ *     (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ * with the angle positions[t] * inv_freq[i] of pair i < R/2, formed and reduced
+ * in 64 bits so that far positions keep their phase; the pair is (i, i + R/2),
+ * or (2i, 2i + 1) with KDA_F_ROPE_INTERLEAVED.  Elements R..D-1 are only
+ * normalised.  The outputs may be the inputs (same pointer and stride).
+ */
+typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm;
+#define KDA_F_ROPE_INTERLEAVED 512u
+
+typedef struct {
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int32_t num_q_heads;     /* >= 1 */
+    int32_t num_k_heads;     /* >= 0; 0 with k = k_out = NULL */
+    int32_t head_dim;        /* D: 64 or 128 */
+    int32_t rotary_dim;      /* R: a multiple of 16, at most D; 0 = no rotation */
+    kda_dtype dtype;
+    kda_norm norm;
+    uint32_t flags;          /* 0 or KDA_F_ROPE_INTERLEAVED */
+    float eps;               /* > 0 */
+    int64_t q_stride, k_stride;         /* elements per token, 0 = dense */
+    int64_t q_out_stride, k_out_stride;
+    const void *q, *k;       /* [T][Hq][D], [T][Hk][D] */
+    void *q_out, *k_out;
+    const float *q_weight, *k_weight;   /* [D] or NULL; KDA_NORM_RMS only */
+    const int32_t *positions;           /* [T] device; NULL exactly when R is 0 */
+    const float *inv_freq;              /* [R/2] device; NULL exactly when R is 0 */
+} kda_qk_norm_rope_args;
+
+kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args *args, hipStream_t stream);
+
+/*
+ * kda_gated_norm -- the mixer's output stage (after kda_prefill, kda_decode or
+ * the linear attention above): per token and head, x of D elements,
+ *     y = w * x / sqrt(|x|^2 / D + eps) * act(z)
+ * act is the logistic function, or z times it with KDA_F_SILU; z = NULL leaves
+ * the factor out.  y may be x or z (same pointer and stride).
+ */
+#define KDA_F_WEIGHT_PER_HEAD 1024u
+
+typedef struct {
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int32_t num_heads;       /* >= 1 */
+    int32_t head_dim;        /* D: 64 or 128 */
+    kda_dtype dtype;
+    uint32_t flags;          /* KDA_F_SILU, KDA_F_WEIGHT_PER_HEAD */
+    float eps;               /* > 0 */
+    int64_t x_stride, z_stride, y_stride; /* elements per token, 0 = dense */
+    const void *x;           /* [T][H][D] */
+    const void *z;           /* [T][H][D] gate pre-activation, or NULL */
+    const float *weight;     /* [D] ([H][D] with KDA_F_WEIGHT_PER_HEAD), or NULL */
+    void *y;                 /* [T][H][D] */
+} kda_gated_norm_args;
+
+kda_status kda_gated_norm(const kda_gated_norm_args *args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
