@@ -65,6 +65,7 @@ hipError_t launch_prefill_fused(const kda_prefill_args *a, hipStream_t s);
 
 // Linear attention with one decay per head; strides and scale are resolved.
 hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t s);
+hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, hipStream_t s);  // bf16 tokens
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s);
 
 // Per-head norms: queries and keys with their rotation, and the gated output norm.

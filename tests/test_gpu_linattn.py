@@ -40,6 +40,22 @@ def test_prefill_head_dims_and_types(dk, dv, dtype, state_dtype):
     check_linattn(o, st, inp, True)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_many_pairs(dk, dv, dtype):
+    """Enough (sequence, head) pairs to fill the GPU without splitting states."""
+    lengths = [(37 * i) % 150 for i in range(17)] + [0, 1, 64, 128, 200]
+    inp = make_linattn(lengths, 16, 8, dk, dv, dtype, seed=40, device=DEV)
+    o, st = _prefill(inp)
+    check_linattn(o, st, inp, True)
+    inp["v"][60, 3, 5] = float("nan")
+    o1, _ = _prefill(inp)
+    keep = torch.ones(o.shape[:2], dtype=torch.bool, device=DEV)
+    assert lengths[0] == 0 and lengths[1] == 37 and lengths[2] == 74
+    keep[60:111, 3] = False  # the third sequence: tokens 37..110
+    assert torch.equal(o[keep], o1[keep]) and not torch.isfinite(o1[60:111, 3].float()).all(-1).any()
+
+
 @pytest.mark.parametrize("H,Hk", [(1, 1), (6, 1), (6, 3), (8, 8), (33, 11)])
 @pytest.mark.parametrize("decay", ["token", "head"])
 def test_prefill_shared_key_heads_and_fixed_decays(H, Hk, decay):
