@@ -9,11 +9,11 @@
 // A workgroup owns DVT columns of one (sequence, head) state and carries it over
 // the chunks in registers.  A wave holds 16 columns of a 1/DKS part of the rows,
 // laid out so that its accumulators, rounded to bf16, are the operand of S^T Q^T
-// as they stand: the state never passes through LDS.  P = K Q^T is formed once,
-// its 16 x 16 blocks shared out over the waves, and reaches them through LDS in
-// operand order.  Two more waves serve the others: one streams q, k, v and g from
-// memory into a ring of LDS stages (LDS DMA, NS - 1 chunks ahead), one turns the
-// decays of the next chunk into the factors above.
+// as they stand: the state never passes through LDS.  P = K Q^T is formed once
+// and reaches the waves through LDS in operand order.  Four more waves serve the others: two stream q, k, v and g from
+// memory into a ring of LDS stages (LDS DMA, NS - 1 chunks ahead; one wave alone
+// would stall at 63 loads in flight and hold the others at their next barrier), two
+// form P and turn the decays of the next chunk into the factors above.
 //
 // Rounding: P and the state under q are rounded to bf16 once as operands (the
 // outputs are bf16 themselves).  The decayed values of the state's own product
@@ -55,11 +55,17 @@ struct ChunkParams {
 // wait for stores and LDS DMA.)
 __device__ __forceinline__ void bar() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Position of 16-byte piece c of row r in a row of CPR pieces: the sixteen rows a
-// wave reads at one piece, and the four rows by four pieces of a transposed read,
-// fall on different banks.
+// Piece c (16 bytes) of row r lies at piece c ^ swz(r) of its row of CPR pieces, with
+// the bits of r permuted so that no two lanes served in one cycle meet in a bank:
+// for q and k a 16-byte read of rows l % 16 at one piece (cycles take l % 16 of
+// 0..3 and 12..15 with the next sixteen lanes' 4..11) and a transposed read of four
+// rows by four pieces' halves, for v the transposed read of two whole pieces.
 template <int CPR> __device__ __forceinline__ int swz(int r) {
-    return CPR == 16 ? ((r & 3) << 2 | (r >> 2 & 3)) : CPR == 8 ? ((r >> 1 & 1) << 2 | (r >> 2 & 3)) : 0;
+    const int lo = CPR == 16 ? (r & 1) | (r >> 1 & 1) << 3 : r >> 1 & 1;
+    return lo | (r >> 3 & 1) << 1 | (r >> 2 & 1) << 2;
+}
+template <int CPR> __device__ __forceinline__ int swz_v(int r) {
+    return CPR == 16 ? (r & 7) << 1 | (r >> 3 & 1) : CPR == 8 ? (r & 6) | (r >> 3 & 1) : (r >> 2 & 1) << 1;
 }
 
 // Transposed read: lane l gets rows 4 (l / 16) + 0..3 of column l % 16, from four
@@ -76,23 +82,23 @@ __device__ __forceinline__ void dma16(unsigned char *dst, const unsigned char *s
 // DMA of the chunk's first n rows of CPR pieces at `src` (rows `stride` bytes apart)
 // into LDS; rows past them repeat the last one, which a zero weight or a row that
 // is not stored makes harmless.
-template <int CPR>
+template <int CPR, bool V, int I0 = 0, int I1 = CPR>  // instructions I0 .. I1 - 1 of CPR
 __device__ __forceinline__ void dma_rows(unsigned char *dst, const unsigned char *src, int64_t stride, int n,
                                          int lane) {
     constexpr int RPI = 64 / CPR;  // rows per instruction
     const int lr = lane / CPR, pc = lane % CPR;
     if (n == C) {
-        const unsigned char *row = src + lr * stride;
+        const unsigned char *row = src + (I0 * RPI + lr) * stride;
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-            dma16(dst + i * 1024, row + (pc ^ swz<CPR>(i * RPI + lr)) * 16);
+        for (int i = I0; i < I1; ++i) {
+            dma16(dst + i * 1024, row + (pc ^ (V ? swz_v<CPR>(i * RPI + lr) : swz<CPR>(i * RPI + lr))) * 16);
             row += RPI * stride;
         }
     } else {
 #pragma unroll 1
-        for (int i = 0; i < CPR; ++i) {
+        for (int i = I0; i < I1; ++i) {
             const int row = i * RPI + lr;
-            dma16(dst + i * 1024, src + (int64_t)min(row, n - 1) * stride + (pc ^ swz<CPR>(row)) * 16);
+            dma16(dst + i * 1024, src + (int64_t)min(row, n - 1) * stride + (pc ^ (V ? swz_v<CPR>(row) : swz<CPR>(row))) * 16);
         }
     }
 }
@@ -125,41 +131,71 @@ __device__ __forceinline__ bool locate(const ChunkParams &p, Work &w) {
 
 template <int DK, int DVT, int DKS, int NS> struct Lay {
     static constexpr int NCT = DVT / 16, NW = NCT * DKS;  // column tiles, compute waves
-    static constexpr int STAGES = NS;
-    static constexpr int UD = DK / 32 / DKS;              // 32-row groups of the state per wave
+    static constexpr int STAGES = NS, UD = DK / 32 / DKS; // 32-row groups of the state per wave
     static constexpr int QB = C * DK * 2, VB = C * DVT * 2, STAGE = 2 * QB + VB;
     static constexpr int CPR = DK / 8, CPV = DVT / 8;     // 16-byte pieces of a row
     static constexpr int G = NS * STAGE;                  // ring of raw decays
-    static constexpr int P = G + NS * 256;                // P, six operand pairs of 1 KiB
-    static constexpr int B = P + 6144;                    // decay factors, two chunks
-    static constexpr int X = B + 2 * 1040;                // partial outputs when DKS > 1
-    static constexpr int TOTAL = X + (DKS > 1 ? NCT * 4 * DKS * 1024 : 0);
-    static constexpr int THREADS = (NW + 2) * 64;
-    static constexpr int DMAS = STAGE / 1024 + 1;         // DMA instructions per chunk
+    static constexpr int P = G + NS * 256;                // P of two chunks, six operand pairs of 1 KiB each
+    static constexpr int B = P + 2 * 6144;                // decay factors of three chunks
+    static constexpr int X = B + 3 * 1040;                // partial outputs of two chunks when DKS > 1
+    static constexpr int XB = DKS > 1 ? NCT * 4 * DKS * 1024 : 0;
+    static constexpr int TOTAL = X + 2 * XB;
+    static constexpr int THREADS = (NW + 4) * 64;
+    static constexpr int DMAS = CPR + CPV / 2;            // DMA instructions per chunk and streaming wave
     static_assert(UD >= 1 && TOTAL <= 160 * 1024, "LDS");
 };
 
-// The streaming wave's view of its sequence and head (strides in bytes, g's in
-// elements).
+// A streaming wave's view of its sequence and head (strides in bytes, g's in
+// elements): the first takes q, g and the upper half of v, the second k and the rest.
 struct Stream {
-    const unsigned char *q, *k, *v;
+    const unsigned char *x, *v;
     const float *g;
-    int64_t qs, ks, vs, gs;
+    int64_t xs, vs, gs;
     int len, nc;
 };
+// (One past the last chunk is fetched too, from its last token, so that every chunk
+// comes with the same number of loads.)
 template <typename L> __device__ __forceinline__ void fetch_g(const Stream &m, unsigned char *lds, int c, int lane) {
-    if (c < m.nc)
+    if (c <= m.nc)
         __builtin_amdgcn_global_load_lds(m.g + (int64_t)min(c * C + lane, m.len - 1) * m.gs,
                                          (lds_void *)(lds + L::G + (c % L::STAGES) * 256), 4, 0, 0);
 }
-template <typename L> __device__ __forceinline__ void fetch(const Stream &m, unsigned char *lds, int c, int lane) {
+template <typename L, int SW>
+__device__ __forceinline__ void fetch(const Stream &m, unsigned char *lds, int c, int lane) {
     if (c >= m.nc) return;
     unsigned char *st = lds + (c % L::STAGES) * L::STAGE;
     const int n = min(m.len - c * C, C);
     const int64_t t = (int64_t)c * C;
-    dma_rows<L::CPR>(st, m.q + t * m.qs, m.qs, n, lane);
-    dma_rows<L::CPR>(st + L::QB, m.k + t * m.ks, m.ks, n, lane);
-    dma_rows<L::CPV>(st + 2 * L::QB, m.v + t * m.vs, m.vs, n, lane);
+    dma_rows<L::CPR, false>(st + SW * L::QB, m.x + t * m.xs, m.xs, n, lane);
+    dma_rows<L::CPV, true, SW * L::CPV / 2, (SW + 1) * L::CPV / 2>(st + 2 * L::QB, m.v + t * m.vs, m.vs, n, lane);
+}
+template <typename L, int SW>
+__device__ __forceinline__ void stream(const Stream &m, unsigned char *lds, int lane) {
+    constexpr int NS = L::STAGES, EACH = L::DMAS + (SW == 0);
+    // issued in order g0, then (g of chunk c + 1, chunk c): when chunk c has
+    // landed, so has the next chunk's g
+    if (SW == 0) fetch_g<L>(m, lds, 0, lane);
+    auto next = [&](int c) __attribute__((always_inline)) {
+        if (SW == 0) fetch_g<L>(m, lds, c + 1, lane);
+        fetch<L, SW>(m, lds, c, lane);
+    };
+    // chunk c has landed when only the chunks behind it are outstanding
+    auto landed = [&](int c, auto behind) __attribute__((always_inline)) {
+        constexpr int N = decltype(behind)::value * EACH;
+        static_assert(N + EACH < 64, "loads in flight");
+        if (c + decltype(behind)::value < m.nc) wait_vmcnt<N>();
+        else wait_vmcnt<0>();
+    };
+    for (int c = 0; c < NS - 1; ++c) next(c);
+    landed(0, std::integral_constant<int, NS - 2>{});
+    bar();
+    next(NS - 1);
+    bar();
+    for (int c = 0; c < m.nc; ++c) {
+        landed(c + 1, std::integral_constant<int, NS - 2>{});
+        bar();  // c: the slot of chunk c is free, chunk c + 1 is there
+        next(c + NS);
+    }
 }
 
 // Factors of one chunk: bh + bl (the decay sums, base 2), eb = 2^b, w = 2^(b_n - b)
@@ -168,23 +204,56 @@ struct Factors {
     float bh[C], bl[C], eb[C], w[C], total, pad[3];
 };
 
+// DPP move of a double, zero where a lane has no source or its row is masked off.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_f64(double x) {
+    typedef __attribute__((ext_vector_type(2))) int i32x2;
+    const i32x2 v = __builtin_bit_cast(i32x2, x);
+    i32x2 r;
+    r.x = __builtin_amdgcn_update_dpp(0, v.x, CTRL, ROWS, 0xf, false);
+    r.y = __builtin_amdgcn_update_dpp(0, v.y, CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, r);
+}
+__device__ __forceinline__ double lane63_f64(double x) {
+    typedef __attribute__((ext_vector_type(2))) int i32x2;
+    i32x2 v = __builtin_bit_cast(i32x2, x);
+    v.x = __builtin_amdgcn_readlane(v.x, 63);
+    v.y = __builtin_amdgcn_readlane(v.y, 63);
+    return __builtin_bit_cast(double, v);
+}
+
 __device__ __forceinline__ void chunk_factors(const float *g, Factors *f, int n, int lane) {
     float x = g[lane];
     x = x > 0.f ? 0.f : x;                   // NaN stays
     x = x < -1e6f ? -1e6f : x;               // 2^(-1e6) is 0 as well; sums stay finite
     double b = lane < n ? (double)x * 1.4426950408889634 : 0.0;
-#pragma unroll
-    for (int d = 1; d < C; d *= 2) {
-        const double y = __shfl_up(b, d);
-        if (lane >= d) b += y;
-    }
-    const double e = __shfl(b, C - 1);
+    b += dpp_f64<0x111, 0xf>(b);  // row_shr 1, 2, 4, 8: sums inside 16 lanes
+    b += dpp_f64<0x112, 0xf>(b);
+    b += dpp_f64<0x114, 0xf>(b);
+    b += dpp_f64<0x118, 0xf>(b);
+    b += dpp_f64<0x142, 0xa>(b);  // lane 15 and 47 into the next 16
+    b += dpp_f64<0x143, 0xc>(b);  // lane 31 into the upper half
+    const double e = lane63_f64(b);
     const float hi = (float)b;
     f->bh[lane] = hi;
     f->bl[lane] = (float)(b - (double)hi);
     f->eb[lane] = exp2_fast(hi);
     f->w[lane] = lane < n ? exp2_fast((float)(e - b)) : 0.f;
     if (lane == 0) f->total = exp2_fast((float)e);
+}
+
+// x = a + b + c exactly, each the upper half of its word a bf16 (8 bits of x's 24).
+__device__ __forceinline__ void split3(float x, uint32_t &a, uint32_t &b, uint32_t &c) {
+    a = __builtin_bit_cast(uint32_t, x);
+    const float y = x - __builtin_bit_cast(float, a & 0xffff0000u);
+    b = __builtin_bit_cast(uint32_t, y);
+    c = __builtin_bit_cast(uint32_t, y - __builtin_bit_cast(float, b & 0xffff0000u));
+}
+__device__ __forceinline__ bf16x8 upper_halves(const uint32_t *x) {
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
+    return __builtin_bit_cast(bf16x8, r);
 }
 
 __device__ __forceinline__ bool has_non_finite(bf16x8 a, bf16x8 b) {
@@ -194,6 +263,45 @@ __device__ __forceinline__ bool has_non_finite(bf16x8 a, bf16x8 b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r = max(r, (unsigned)x[i]);
     return r >= 0x7f80;
+}
+
+// Five of the ten 16 x 16 blocks of P at or below the diagonal: row blocks 0..2 against
+// key blocks 0 and 1, or (2, 2) and the last row block.  Lane: token 16 rt + l % 16,
+// keys 16 st + 4 (l / 16) + 0..3, the operand order of V^T P^T.
+template <int DK, int HALF>
+__device__ __forceinline__ void scores(const unsigned char *lq, const unsigned char *lk, const Factors *f,
+                                       unsigned char *pl, int lane) {
+    constexpr int RT[2][5] = {{0, 1, 1, 2, 2}, {2, 3, 3, 3, 3}}, ST[2][5] = {{0, 0, 1, 0, 1}, {2, 0, 1, 2, 3}};
+    const int r16 = lane & 15, g4 = lane >> 4, frow = swz<DK / 8>(r16);
+    f32x4 d[5];
+#pragma unroll
+    for (int b = 0; b < 5; ++b) d[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < DK / 32; ++u) {
+        const int off = r16 * (DK * 2) + ((4 * u + g4) ^ frow) * 16;
+        bf16x8 q[4], k[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (HALF ? t >= 2 : t < 3) q[t] = *reinterpret_cast<const bf16x8 *>(lq + 16 * t * (DK * 2) + off);
+            if (HALF || t < 2) k[t] = *reinterpret_cast<const bf16x8 *>(lk + 16 * t * (DK * 2) + off);
+        }
+#pragma unroll
+        for (int b = 0; b < 5; ++b) d[b] = mma_k32(k[ST[HALF][b]], q[RT[HALF][b]], d[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+        const int rt = RT[HALF][b], st = ST[HALF][b], s = 16 * st + 4 * g4;
+        const float rh = f->bh[16 * rt + r16], rl = f->bl[16 * rt + r16];
+        const f32x4 sh = *reinterpret_cast<const f32x4 *>(f->bh + s), sl = *reinterpret_cast<const f32x4 *>(f->bl + s);
+        f32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = d[b][i] * exp2_fast((rh - sh[i]) + (rl - sl[i]));
+            if (rt == st) x[i] = r16 >= 4 * g4 + i ? x[i] : 0.f;
+        }
+        const int pair = (rt < 2 ? rt : 2 * rt - 2) + (st >> 1);
+        *reinterpret_cast<bf16x4 *>(pl + pair * 1024 + lane * 16 + (st & 1) * 8) = pack4(x);
+    }
 }
 
 // acc += V^T P^T of row block rt when the values hold a non-finite one: earlier
@@ -232,50 +340,41 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nc = (wk.len + C - 1) / C;
 
-    if (wave == L::NW) {  // the streaming wave: it reads no LDS
-        const int hk = wk.h / p.rep;
-        Stream sm;
-        sm.q = static_cast<const unsigned char *>(p.q) + ((int64_t)wk.t0 * p.qs + hk * DK) * 2;
-        sm.k = static_cast<const unsigned char *>(p.k) + ((int64_t)wk.t0 * p.ks + hk * DK) * 2;
-        sm.v = static_cast<const unsigned char *>(p.v) +
-               ((int64_t)wk.t0 * p.vs + (int64_t)wk.h * p.dv + wk.tile * DVT) * 2;
-        sm.g = p.g + wk.t0 * p.gs + wk.h;
-        sm.qs = p.qs * 2; sm.ks = p.ks * 2; sm.vs = p.vs * 2; sm.gs = p.gs;
-        sm.len = wk.len; sm.nc = nc;
-        // issued in order g0, then (g of chunk c + 1, chunk c): when chunk c has
-        // landed, so has the next chunk's g
-        fetch_g<L>(sm, lds, 0, lane);
-        for (int c = 0; c < NS - 1; ++c) {
-            fetch_g<L>(sm, lds, c + 1, lane);
-            fetch<L>(sm, lds, c, lane);
-        }
-        for (int c = 0; c < nc; ++c) {
-            // chunk c has landed when only the NS - 2 chunks behind it are outstanding
-            constexpr int AHEAD = (NS - 2) * L::DMAS;
-            if (c + NS - 1 < nc) wait_vmcnt<(AHEAD < 63 ? AHEAD : 63)>();
-            else wait_vmcnt<0>();
-            if (c == 0) bar();  // g0 is there: its factors are formed now
-            bar();  // A
-            fetch_g<L>(sm, lds, c + NS, lane);
-            fetch<L>(sm, lds, c + NS - 1, lane);
-            bar();  // B
-            if (DKS > 1) bar();  // C
-        }
+    // Barriers: one when chunk 0 has landed, one when its factors are formed, then one
+    // at the end of every interval c, in which chunk c is worked on.
+    if (wave >= L::NW && nc == 0) return;
+    if (wave >= L::NW + 2) {  // the streaming waves: they read no LDS
+        const int hk = wk.h / p.rep, sw = wave - L::NW - 2;
+        Stream m;
+        m.xs = (sw ? p.ks : p.qs) * 2; m.vs = p.vs * 2; m.gs = p.gs;
+        m.x = static_cast<const unsigned char *>(sw ? p.k : p.q) + wk.t0 * m.xs + (int64_t)hk * DK * 2;
+        m.v = static_cast<const unsigned char *>(p.v) + wk.t0 * m.vs + ((int64_t)wk.h * p.dv + wk.tile * DVT) * 2;
+        m.g = p.g + wk.t0 * p.gs + wk.h;
+        m.len = wk.len; m.nc = nc;
+        if (sw == 0) stream<L, 0>(m, lds, lane);
+        else stream<L, 1>(m, lds, lane);
         return;
     }
     Factors *fac = reinterpret_cast<Factors *>(lds + L::B);
-    if (wave == L::NW + 1) {  // the decay wave
+    if (wave >= L::NW) {  // the score waves; the first also forms the factors of chunk c + 1
+        auto form = [&](int c) __attribute__((always_inline)) {
+            if (c < nc)
+                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % NS) * 256), fac + c % 3,
+                              min(wk.len - c * C, C), lane);
+        };
+        bar();
+        if (wave == L::NW) form(0);
+        bar();
         for (int c = 0; c < nc; ++c) {
-            if (c == 0) {
-                bar();
-                chunk_factors(reinterpret_cast<const float *>(lds + L::G), fac, min(wk.len, C), lane);
+            const unsigned char *lq = lds + (c % NS) * L::STAGE;
+            unsigned char *pl = lds + L::P + (c & 1) * 6144;
+            if (wave == L::NW) {
+                scores<DK, 0>(lq, lq + L::QB, fac + c % 3, pl, lane);
+                form(c + 1);
+            } else {
+                scores<DK, 1>(lq, lq + L::QB, fac + c % 3, pl, lane);
             }
-            bar();  // A
-            if (c + 1 < nc)
-                chunk_factors(reinterpret_cast<const float *>(lds + L::G + ((c + 1) % NS) * 256), fac + ((c + 1) & 1),
-                              min(wk.len - (c + 1) * C, C), lane);
-            bar();  // B
-            if (DKS > 1) bar();  // C
+            bar();
         }
         return;
     }
@@ -283,7 +382,8 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
     const int r16 = lane & 15, g4 = lane >> 4;
     const int ct = wave % L::NCT, hh = wave / L::NCT;
     const int col = wk.tile * DVT + 16 * ct;
-    // S[u][e][i]: row 32 (hh UD + u) + 8 g4 + 4 e + i, column col + r16
+    // S[u][e][i]: row 32 (hh UD + u) + 8 g4 + 4 (e ^ g4 % 2) + i, column col + r16 (the
+    // exchanged halves keep the transposed reads of k off each other's banks)
     f32x4 S[L::UD][2];
     const size_t sbase = ((size_t)slot * p.H + wk.h) * DK * p.dv + (size_t)(32 * hh * L::UD + 8 * g4) * p.dv + col + r16;
 #pragma unroll
@@ -292,7 +392,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const size_t at = sbase + (size_t)(32 * u + 4 * e + i) * p.dv;
+                const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
                 S[u][e][i] = !p.s_in ? 0.f
                              : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
                                             : static_cast<const float *>(p.s_in)[at];
@@ -300,148 +400,140 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
 
     __bf16 *o = static_cast<__bf16 *>(p.o) + ((size_t)wk.t0 * p.H + wk.h) * p.dv + col + 4 * g4;
     const size_t orow = (size_t)p.H * p.dv;
-    unsigned char *pl = lds + L::P;
-    const int frow = swz<L::CPR>(r16);
-    for (int c = 0; c < nc; ++c) {
-        const unsigned char *lq = lds + (c % NS) * L::STAGE, *lk = lq + L::QB, *lv = lk + L::QB;
-        const Factors *f = fac + (c & 1);
-        const int n = min(wk.len - c * C, C);
-        if (c == 0) bar();
-        bar();  // A: chunk c and its factors are in LDS
-        for (int b = wave; b < 10; b += L::NW) {
-            const int rt = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0, st = b - rt * (rt + 1) / 2;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < DK / 32; ++u) {
-                const int off = ((4 * u + g4) ^ frow) * 16;
-                acc = mma_k32(*reinterpret_cast<const bf16x8 *>(lk + (16 * st + r16) * (DK * 2) + off),
-                              *reinterpret_cast<const bf16x8 *>(lq + (16 * rt + r16) * (DK * 2) + off), acc);
-            }
-            // lane: token r = 16 rt + r16, keys s = 16 st + 4 g4 + i
-            const int r = 16 * rt + r16, s = 16 * st + 4 * g4;
-            const float rh = f->bh[r], rl = f->bl[r];
-            const f32x4 sh = *reinterpret_cast<const f32x4 *>(f->bh + s), sl = *reinterpret_cast<const f32x4 *>(f->bl + s);
-            f32x4 pv;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = acc[i] * exp2_fast((rh - sh[i]) + (rl - sl[i]));
-                pv[i] = r >= s + i ? x : 0.f;
-            }
-            const int pair = (rt < 2 ? rt : 2 * rt - 2) + (st >> 1);
-            *reinterpret_cast<bf16x4 *>(pl + pair * 1024 + lane * 16 + (st & 1) * 8) = pack4(pv);
-        }
-        bar();  // B: P is in LDS
-        bf16x4 vt[4];
-        {
-            const int row = 4 * g4 + (r16 >> 2);
-            const int off = ((2 * ct + (r16 >> 1 & 1)) ^ swz<L::CPV>(row)) * 16 + (r16 & 1) * 8;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) vt[t] = read_tr(lv + (16 * t + row) * (DVT * 2) + off);
-        }
-        const bool odd = __any(has_non_finite(join8(vt[0], vt[1]), join8(vt[2], vt[3])));
-        bf16x8 sb[L::UD];
-#pragma unroll
-        for (int u = 0; u < L::UD; ++u) sb[u] = join8(pack4(S[u][0]), pack4(S[u][1]));
-        const float tot = f->total;
+    const int frow = swz<L::CPR>(r16), trow = 4 * g4 + (r16 >> 2), ftr = swz<L::CPR>(trow);
+    const int voff = trow * (DVT * 2) + ((2 * ct + (r16 >> 1 & 1)) ^ swz_v<L::CPV>(trow)) * 16 + (r16 & 1) * 8;
 
-        // partial S^T q of the row block (this wave's part of the state rows)
-        auto inter = [&](int rt) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    bf16x4 vt[4];     // the chunk's values: column r16, tokens 16 t + 4 g4 + i
+    f32x4 acc[4];     // S^T q of row block t, decayed (DKS 1)
+    bool odd = false; // a value is not finite
+
+    // Interval c: everything of chunk c that needs no other wave.
+    auto own_part = [&](int c) __attribute__((always_inline)) {
+        const unsigned char *lq = lds + (c % NS) * L::STAGE, *lk = lq + L::QB, *lv = lk + L::QB;
+        const Factors *f = fac + c % 3;
 #pragma unroll
-            for (int u = 0; u < L::UD; ++u)
-                acc = mma_k32(sb[u], *reinterpret_cast<const bf16x8 *>(
-                                         lq + (16 * rt + r16) * (DK * 2) + ((4 * (hh * L::UD + u) + g4) ^ frow) * 16), acc);
-            return acc;
-        };
-        // the decayed partial sum, P's part, the store
-        auto finish = [&](int rt, f32x4 acc, auto guarded) {
-            const int r = 16 * rt + r16;
-            acc = acc * f->eb[r];
-            const unsigned char *pr = pl + (rt < 2 ? rt : 2 * rt - 2) * 1024;
-            if constexpr (decltype(guarded)::value) {
-                acc = guarded_pv(acc, vt, pr, rt, lane);
-            } else {
-                const bf16x8 p0 = *reinterpret_cast<const bf16x8 *>(pr + lane * 16);
-                const bf16x4 p0l = {p0[0], p0[1], p0[2], p0[3]};
-                if (rt == 0) {
-                    acc = mma_k16w(vt[0], p0l, acc);
-                } else {
-                    acc = mma_k32(join8(vt[0], vt[1]), p0, acc);
-                    if (rt >= 2) {
-                        const bf16x8 p1 = *reinterpret_cast<const bf16x8 *>(pr + 1024 + lane * 16);
-                        const bf16x4 p1l = {p1[0], p1[1], p1[2], p1[3]};
-                        acc = rt == 2 ? mma_k16w(vt[2], p1l, acc) : mma_k32(join8(vt[2], vt[3]), p1, acc);
-                    }
-                }
-            }
-            if (r < n) *reinterpret_cast<bf16x4 *>(o + (size_t)(c * C + r) * orow) = pack4(acc * p.scale);
-        };
-        auto update = [&]() {
+        for (int t = 0; t < 4; ++t) vt[t] = read_tr(lv + 16 * t * (DVT * 2) + voff);
+        // S^T q over this wave's rows, four row blocks side by side
 #pragma unroll
-            for (int u = 0; u < L::UD; ++u)
+        for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) S[u][e] = S[u][e] * tot;
+        for (int u = 0; u < L::UD; ++u) {
+            const bf16x4 s0 = pack4(S[u][0]), s1 = pack4(S[u][1]);
+            const bf16x8 sb = (g4 & 1) ? join8(s1, s0) : join8(s0, s1);
+            const unsigned char *qr = lq + r16 * (DK * 2) + ((4 * (hh * L::UD + u) + g4) ^ frow) * 16;
 #pragma unroll
-            for (int kp = 0; kp < 2; ++kp) {
-                bf16x8 v3[3];
+            for (int t = 0; t < 4; ++t)
+                acc[t] = mma_k32(sb, *reinterpret_cast<const bf16x8 *>(qr + 16 * t * (DK * 2)), acc[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = acc[t] * f->eb[16 * t + r16];
+        if constexpr (DKS > 1) {
+            f32x4 *xs = reinterpret_cast<f32x4 *>(lds + L::X + (c & 1) * L::XB) + (size_t)ct * 4 * DKS * 64;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) xs[(t * DKS + hh) * 64 + lane] = acc[t];
+        }
+        odd = __any(has_non_finite(join8(vt[0], vt[1]), join8(vt[2], vt[3])));
+        // the state over the chunk: K^T V' with V' in three exact parts
+        const float tot = f->total;
+#pragma unroll
+        for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) S[u][e] = S[u][e] * tot;
+#pragma unroll
+        for (int kp = 0; kp < 2; ++kp) {
+            bf16x8 v3[3];
+            {
+                uint32_t x[8], y[8], z[8];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const f32x4 w = *reinterpret_cast<const f32x4 *>(f->w + 32 * kp + 16 * t + 4 * g4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = (float)vt[2 * kp + t][i] * w[i];
-                        const __bf16 a = (__bf16)x;
-                        const float y = x - (float)a;
-                        const __bf16 b = (__bf16)y;
-                        v3[0][4 * t + i] = a;
-                        v3[1][4 * t + i] = b;
-                        v3[2][4 * t + i] = (__bf16)(y - (float)b);
-                    }
+                    for (int i = 0; i < 4; ++i) split3((float)vt[2 * kp + t][i] * w[i], x[4 * t + i], y[4 * t + i], z[4 * t + i]);
                 }
-                const int row = 4 * g4 + (r16 >> 2), sw = swz<L::CPR>(row);
+                v3[0] = upper_halves(x);
+                v3[1] = upper_halves(y);
+                v3[2] = upper_halves(z);
+            }
 #pragma unroll
-                for (int u = 0; u < L::UD; ++u)
+            for (int u0 = 0; u0 < L::UD; u0 += 2) {
+                constexpr int W = L::UD < 2 ? 1 : 2;
+                bf16x8 kt[W][2];
+#pragma unroll
+                for (int u = 0; u < W; ++u)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const unsigned char *kr = lk + (32 * kp + row) * (DK * 2) +
-                                                  ((4 * (hh * L::UD + u) + (r16 & 3)) ^ sw) * 16 + 8 * e;
-                        const bf16x8 kt = join8(read_tr(kr), read_tr(kr + 16 * DK * 2));
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) S[u][e] = mma_k32(kt, v3[i], S[u][e]);
+                        const unsigned char *kr = lk + (32 * kp + trow) * (DK * 2) +
+                                                  ((4 * (hh * L::UD + u0 + u) + (r16 & 3)) ^ ftr) * 16 + 8 * (e ^ (r16 & 1));
+                        kt[u][e] = join8(read_tr(kr), read_tr(kr + 16 * DK * 2));
                     }
-                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int u = 0; u < W; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) S[u0 + u][e] = mma_k32(kt[u][e], v3[i], S[u0 + u][e]);
             }
-        };
+        }
+    };
+    // Behind barrier c: P's part of a row block, and its store (only the last chunk can
+    // end early).
+    auto finish = [&](int c, int rt, f32x4 d, auto guarded, auto last) __attribute__((always_inline)) {
+        const unsigned char *pr = lds + L::P + (c & 1) * 6144 + (rt < 2 ? rt : 2 * rt - 2) * 1024;
+        if constexpr (decltype(guarded)::value) {
+            d = guarded_pv(d, vt, pr, rt, lane);
+        } else {
+            // a half pair past the diagonal drops out on both sides
+            const bf16x4 z = {};
+            const bf16x8 p0 = *reinterpret_cast<const bf16x8 *>(pr + lane * 16);
+            const bf16x4 a0 = {p0[0], p0[1], p0[2], p0[3]}, a1 = {p0[4], p0[5], p0[6], p0[7]};
+            d = mma_k32(join8(vt[0], rt >= 1 ? vt[1] : z), join8(a0, rt >= 1 ? a1 : z), d);
+            if (rt >= 2) {
+                const bf16x8 p1 = *reinterpret_cast<const bf16x8 *>(pr + 1024 + lane * 16);
+                const bf16x4 b0 = {p1[0], p1[1], p1[2], p1[3]}, b1 = {p1[4], p1[5], p1[6], p1[7]};
+                d = mma_k32(join8(vt[2], rt >= 3 ? vt[3] : z), join8(b0, rt >= 3 ? b1 : z), d);
+            }
+        }
+        const int t = c * C + 16 * rt + r16;
+        if (!decltype(last)::value || t < wk.len)
+            *reinterpret_cast<bf16x4 *>(o + (size_t)t * orow) = pack4(d * p.scale);
+    };
+    auto outputs = [&](int c, auto guarded, auto last) __attribute__((always_inline)) {
         if constexpr (DKS == 1) {
-            if (odd) {
+            if constexpr (decltype(guarded)::value) {
 #pragma unroll 1
-                for (int rt = 0; rt < 4; ++rt) finish(rt, inter(rt), std::true_type{});
+                for (int rt = 0; rt < 4; ++rt)
+                    finish(c, rt, rt == 0 ? acc[0] : rt == 1 ? acc[1] : rt == 2 ? acc[2] : acc[3], guarded, last);
             } else {
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    finish(rt, inter(rt), std::false_type{});
-                    __builtin_amdgcn_sched_barrier(0);  // operands of one row block at a time
-                }
+                for (int rt = 0; rt < 4; ++rt) finish(c, rt, acc[rt], guarded, last);
             }
-            update();
         } else {
             // row block rt of column tile ct is finished by one of its DKS waves, from
             // the partial sums of all of them in order
-            f32x4 *xs = reinterpret_cast<f32x4 *>(lds + L::X) + (size_t)ct * 4 * DKS * 64;
+            const f32x4 *xs = reinterpret_cast<const f32x4 *>(lds + L::X + (c & 1) * L::XB) + (size_t)ct * 4 * DKS * 64;
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) xs[(rt * DKS + hh) * 64 + lane] = inter(rt);
-            update();
-            bar();  // C: the partial sums are in LDS
-#pragma unroll 1
             for (int j = 0; j < 4 / DKS; ++j) {
                 const int rt = DKS == 4 ? hh : (j == 0 ? hh : 3 - hh);
-                f32x4 acc = xs[rt * DKS * 64 + lane];
+                f32x4 d = xs[rt * DKS * 64 + lane];
 #pragma unroll
-                for (int d = 1; d < DKS; ++d) acc = acc + xs[(rt * DKS + d) * 64 + lane];
-                if (odd) finish(rt, acc, std::true_type{});
-                else finish(rt, acc, std::false_type{});
+                for (int i = 1; i < DKS; ++i) d = d + xs[(rt * DKS + i) * 64 + lane];
+                finish(c, rt, d, guarded, last);
             }
         }
+    };
+    if (nc > 0) {
+        bar();
+        bar();
+        own_part(0);
+        bar();
+        for (int c = 1; c < nc; ++c) {
+            if (odd) outputs(c - 1, std::true_type{}, std::false_type{});
+            else outputs(c - 1, std::false_type{}, std::false_type{});
+            own_part(c);
+            bar();
+        }
+        if (odd) outputs(nc - 1, std::true_type{}, std::true_type{});
+        else outputs(nc - 1, std::false_type{}, std::true_type{});
     }
     if (!p.s_out) return;
 #pragma unroll
@@ -450,7 +542,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const size_t at = sbase + (size_t)(32 * u + 4 * e + i) * p.dv;
+                const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
                 if (p.state_bf16) static_cast<__bf16 *>(p.s_out)[at] = (__bf16)S[u][e][i];
                 else static_cast<float *>(p.s_out)[at] = S[u][e][i];
             }
