@@ -63,9 +63,16 @@ hipError_t launch_prefill_split(const kda_prefill_args *a, int dv_tile, const Sp
 // Fused schedule: one workgroup per (sequence, head), no workspace.
 hipError_t launch_prefill_fused(const kda_prefill_args *a, hipStream_t s);
 
-// Linear attention with one decay per head; strides and scale are resolved.
-hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t s);
-hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, hipStream_t s);  // bf16 tokens
+// Linear attention with one decay per head; strides and scale are resolved.  The
+// plan cuts the sequences into segments that share the workspace.
+struct LinattnPlan {
+    int tokens;        // tokens per segment, 0: whole sequences
+    int64_t segments;  // segment numbers, and the workspace they need
+    size_t bytes;
+};
+hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s);
+hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan,
+                                 hipStream_t s);  // bf16 tokens
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s);
 
 // Per-head norms: queries and keys with their rotation, and the gated output norm.

@@ -15,6 +15,12 @@
 // would stall at 63 loads in flight and hold the others at their next barrier), two
 // form P and turn the decays of the next chunk into the factors above.
 //
+// With few (sequence, head) pairs the sequences are cut into segments, and three
+// launches spread them over the GPU: every segment's state from nothing (the same
+// kernel without q, P and outputs), a scan of those states along each sequence, and
+// the outputs with every segment starting from its scanned state.  The keys and
+// values are read twice for it.
+//
 // Rounding: P and the state under q are rounded to bf16 once as operands (the
 // outputs are bf16 themselves).  The decayed values of the state's own product
 // are split into three bf16 parts, which hold an fp32 value exactly, because the
@@ -49,6 +55,10 @@ struct ChunkParams {
     int N, H, rep, num_slots, dv, tiles, units;
     int state_bf16;
     float scale;
+    // segments: tokens in each (0: whole sequences), their number, the states they
+    // start from in accumulator order and their decay products, both [segment][head]
+    int seg, segs;
+    float *ws, *wdec;
 };
 
 // Workgroup barrier behind this wave's own LDS accesses.  (A fence would also
@@ -103,50 +113,83 @@ __device__ __forceinline__ void dma_rows(unsigned char *dst, const unsigned char
     }
 }
 
-// What a workgroup works on, from its block index.  The rep * tiles workgroups
+// First token of sequence n (n = N: the end of the last one).
+__device__ __forceinline__ int64_t seq_start(const ChunkParams &p, int n) {
+    return p.cu ? min((int64_t)max(p.cu[n], 0), p.total) : p.total / p.N * n;
+}
+
+// Segments are numbered with room for one partial one per sequence: sequence n's
+// begin at seq_start / seg + n, and numbers past its last are unused.
+__device__ __forceinline__ int seg_base(const ChunkParams &p, int n) { return (int)(seq_start(p, n) / p.seg) + n; }
+
+// The sequence that segment number s belongs to: sixty-four probes at a time.
+__device__ __forceinline__ int seg_seq(const ChunkParams &p, int s, int lane) {
+    int lo = 0, cnt = p.N;
+    while (cnt > 1) {
+        const int step = (cnt + 63) / 64, i = lo + lane * step;
+        const bool below = i < lo + cnt && seg_base(p, i) <= s;
+        const int m = __popcll(__ballot(below));
+        lo += m > 1 ? (m - 1) * step : 0;
+        cnt = min(step, p.N - lo);
+    }
+    return lo;
+}
+
+// What a workgroup works on, from its block index: segment s (a whole sequence
+// without segments), number j of its sequence's `nseg`.  The rep * tiles workgroups
 // that read the same keys are `units` neighbours on one XCD (blocks go round the
 // eight XCDs), where they share its L2.
 struct Work {
-    int n, h, tile;
+    int n, h, tile, s, j, nseg;
     int64_t t0;
     int len;
 };
-__device__ __forceinline__ bool locate(const ChunkParams &p, Work &w) {
+__device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) {
     const int U = p.rep * p.tiles, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
     const int unit = (idx / U) * 8 + xcd, member = idx % U;
     if (unit >= p.units) return false;
     const int Hk = p.H / p.rep;
-    w.n = unit / Hk;
-    w.h = (unit - w.n * Hk) * p.rep + member / p.tiles;
+    w.s = unit / Hk;
+    w.h = (unit - w.s * Hk) * p.rep + member / p.tiles;
     w.tile = member % p.tiles;
-    if (p.cu) {
-        w.t0 = min((int64_t)max(p.cu[w.n], 0), p.total);
-        w.len = (int)max(min((int64_t)max(p.cu[w.n + 1], 0), p.total) - w.t0, (int64_t)0);
-    } else {
-        w.len = (int)(p.total / p.N);
-        w.t0 = (int64_t)w.len * w.n;
+    w.n = p.seg ? __builtin_amdgcn_readfirstlane(seg_seq(p, w.s, lane)) : w.s;
+    w.t0 = seq_start(p, w.n);
+    w.len = (int)max(seq_start(p, w.n + 1) - w.t0, (int64_t)0);
+    w.j = 0;
+    w.nseg = 1;
+    if (p.seg) {
+        w.j = w.s - seg_base(p, w.n);
+        w.nseg = max((w.len + p.seg - 1) / p.seg, 1);
+        if (w.j >= w.nseg) return false;
+        w.t0 += (int64_t)w.j * p.seg;
+        w.len = min(w.len - w.j * p.seg, p.seg);
     }
     return true;
 }
 
-template <int DK, int DVT, int DKS, int NS> struct Lay {
+// LDS of a workgroup.  OUT false: the state alone, without q and P.
+template <int DK, int DVT, int DKS, int NS, bool OUT> struct Lay {
     static constexpr int NCT = DVT / 16, NW = NCT * DKS;  // column tiles, compute waves
     static constexpr int STAGES = NS, UD = DK / 32 / DKS; // 32-row groups of the state per wave
-    static constexpr int QB = C * DK * 2, VB = C * DVT * 2, STAGE = 2 * QB + VB;
+    static constexpr bool Q = OUT;
+    static constexpr int QB = C * DK * 2, VB = C * DVT * 2;
+    static constexpr int K = OUT ? QB : 0, V = K + QB, STAGE = V + VB;  // q, k, v in a stage
     static constexpr int CPR = DK / 8, CPV = DVT / 8;     // 16-byte pieces of a row
     static constexpr int G = NS * STAGE;                  // ring of raw decays
     static constexpr int P = G + NS * 256;                // P of two chunks, six operand pairs of 1 KiB each
-    static constexpr int B = P + 2 * 6144;                // decay factors of three chunks
+    static constexpr int B = P + (OUT ? 2 * 6144 : 0);    // decay factors of three chunks
     static constexpr int X = B + 3 * 1040;                // partial outputs of two chunks when DKS > 1
-    static constexpr int XB = DKS > 1 ? NCT * 4 * DKS * 1024 : 0;
+    static constexpr int XB = OUT && DKS > 1 ? NCT * 4 * DKS * 1024 : 0;
     static constexpr int TOTAL = X + 2 * XB;
-    static constexpr int THREADS = (NW + 4) * 64;
-    static constexpr int DMAS = CPR + CPV / 2;            // DMA instructions per chunk and streaming wave
+    static constexpr int SERVE = OUT ? 2 : 1;             // waves that form factors and P
+    static constexpr int THREADS = (NW + SERVE + 2) * 64;
+    static constexpr int DMAS = OUT ? CPR + CPV / 2 : (CPR + CPV) / 2;  // loads per chunk and streaming wave
     static_assert(UD >= 1 && TOTAL <= 160 * 1024, "LDS");
 };
 
 // A streaming wave's view of its sequence and head (strides in bytes, g's in
-// elements): the first takes q, g and the upper half of v, the second k and the rest.
+// elements): the first takes q, g and the upper half of v, the second k and the rest;
+// without q they share k like v.
 struct Stream {
     const unsigned char *x, *v;
     const float *g;
@@ -166,8 +209,9 @@ __device__ __forceinline__ void fetch(const Stream &m, unsigned char *lds, int c
     unsigned char *st = lds + (c % L::STAGES) * L::STAGE;
     const int n = min(m.len - c * C, C);
     const int64_t t = (int64_t)c * C;
-    dma_rows<L::CPR, false>(st + SW * L::QB, m.x + t * m.xs, m.xs, n, lane);
-    dma_rows<L::CPV, true, SW * L::CPV / 2, (SW + 1) * L::CPV / 2>(st + 2 * L::QB, m.v + t * m.vs, m.vs, n, lane);
+    if constexpr (L::Q) dma_rows<L::CPR, false>(st + SW * L::K, m.x + t * m.xs, m.xs, n, lane);
+    else dma_rows<L::CPR, false, SW * L::CPR / 2, (SW + 1) * L::CPR / 2>(st, m.x + t * m.xs, m.xs, n, lane);
+    dma_rows<L::CPV, true, SW * L::CPV / 2, (SW + 1) * L::CPV / 2>(st + L::V, m.v + t * m.vs, m.vs, n, lane);
 }
 template <typename L, int SW>
 __device__ __forceinline__ void stream(const Stream &m, unsigned char *lds, int lane) {
@@ -329,25 +373,27 @@ __device__ __forceinline__ f32x4 guarded_pv(f32x4 acc, const bf16x4 *vt, const u
     return acc;
 }
 
-template <int DK, int DVT, int DKS, int NS>
-__global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel(ChunkParams p) {
-    typedef Lay<DK, DVT, DKS, NS> L;
+template <int DK, int DVT, int DKS, int NS, bool OUT>
+__global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_kernel(ChunkParams p) {
+    typedef Lay<DK, DVT, DKS, NS, OUT> L;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[L::TOTAL];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Work wk;
-    if (!locate(p, wk)) return;
+    if (!locate(p, wk, lane)) return;
+    if (!OUT && wk.j + 1 >= wk.nseg) return;  // nothing starts from the last segment
     const int slot = pool_slot(p.slots, p.num_slots, wk.n);
     if (slot < 0) return;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nc = (wk.len + C - 1) / C;
 
     // Barriers: one when chunk 0 has landed, one when its factors are formed, then one
     // at the end of every interval c, in which chunk c is worked on.
     if (wave >= L::NW && nc == 0) return;
-    if (wave >= L::NW + 2) {  // the streaming waves: they read no LDS
-        const int hk = wk.h / p.rep, sw = wave - L::NW - 2;
+    if (wave >= L::NW + L::SERVE) {  // the streaming waves: they read no LDS
+        const int hk = wk.h / p.rep, sw = wave - L::NW - L::SERVE;
+        const bool keys = sw || !OUT;
         Stream m;
-        m.xs = (sw ? p.ks : p.qs) * 2; m.vs = p.vs * 2; m.gs = p.gs;
-        m.x = static_cast<const unsigned char *>(sw ? p.k : p.q) + wk.t0 * m.xs + (int64_t)hk * DK * 2;
+        m.xs = (keys ? p.ks : p.qs) * 2; m.vs = p.vs * 2; m.gs = p.gs;
+        m.x = static_cast<const unsigned char *>(keys ? p.k : p.q) + wk.t0 * m.xs + (int64_t)hk * DK * 2;
         m.v = static_cast<const unsigned char *>(p.v) + wk.t0 * m.vs + ((int64_t)wk.h * p.dv + wk.tile * DVT) * 2;
         m.g = p.g + wk.t0 * p.gs + wk.h;
         m.len = wk.len; m.nc = nc;
@@ -369,10 +415,10 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
             const unsigned char *lq = lds + (c % NS) * L::STAGE;
             unsigned char *pl = lds + L::P + (c & 1) * 6144;
             if (wave == L::NW) {
-                scores<DK, 0>(lq, lq + L::QB, fac + c % 3, pl, lane);
+                if constexpr (OUT) scores<DK, 0>(lq, lq + L::K, fac + c % 3, pl, lane);
                 form(c + 1);
-            } else {
-                scores<DK, 1>(lq, lq + L::QB, fac + c % 3, pl, lane);
+            } else if constexpr (OUT) {
+                scores<DK, 1>(lq, lq + L::K, fac + c % 3, pl, lane);
             }
             bar();
         }
@@ -386,17 +432,35 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
     // exchanged halves keep the transposed reads of k off each other's banks)
     f32x4 S[L::UD][2];
     const size_t sbase = ((size_t)slot * p.H + wk.h) * DK * p.dv + (size_t)(32 * hh * L::UD + 8 * g4) * p.dv + col + r16;
+    // a segment's starting state: the user's for a sequence in one piece; else the
+    // first segment keeps a copy for the outputs, which may replace the user's
+    const size_t wbase = ((size_t)wk.s * p.H + wk.h) * DK * p.dv + ((size_t)wk.tile * L::NW + wave) * L::UD * 512 + lane * 4;
+    const size_t wnext = (size_t)p.H * DK * p.dv;
+    if (OUT && wk.nseg > 1) {
 #pragma unroll
-    for (int u = 0; u < L::UD; ++u)
+        for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) S[u][e] = *reinterpret_cast<const f32x4 *>(p.ws + wbase + (2 * u + e) * 256);
+    } else {
+        const bool given = p.s_in && wk.j == 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
-                S[u][e][i] = !p.s_in ? 0.f
-                             : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
-                                            : static_cast<const float *>(p.s_in)[at];
-            }
+        for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
+                    S[u][e][i] = !given ? 0.f
+                                 : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
+                                                : static_cast<const float *>(p.s_in)[at];
+                }
+        if (!OUT && wk.j == 0) {
+#pragma unroll
+            for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(p.ws + wbase + (2 * u + e) * 256) = S[u][e];
+        }
+    }
 
     __bf16 *o = static_cast<__bf16 *>(p.o) + ((size_t)wk.t0 * p.H + wk.h) * p.dv + col + 4 * g4;
     const size_t orow = (size_t)p.H * p.dv;
@@ -409,10 +473,11 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
 
     // Interval c: everything of chunk c that needs no other wave.
     auto own_part = [&](int c) __attribute__((always_inline)) {
-        const unsigned char *lq = lds + (c % NS) * L::STAGE, *lk = lq + L::QB, *lv = lk + L::QB;
+        const unsigned char *lq = lds + (c % NS) * L::STAGE, *lk = lq + L::K, *lv = lq + L::V;
         const Factors *f = fac + c % 3;
 #pragma unroll
         for (int t = 0; t < 4; ++t) vt[t] = read_tr(lv + 16 * t * (DVT * 2) + voff);
+        if constexpr (OUT) {
         // S^T q over this wave's rows, four row blocks side by side
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -433,6 +498,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
             for (int t = 0; t < 4; ++t) xs[(t * DKS + hh) * 64 + lane] = acc[t];
         }
         odd = __any(has_non_finite(join8(vt[0], vt[1]), join8(vt[2], vt[3])));
+        }
         // the state over the chunk: K^T V' with V' in three exact parts
         const float tot = f->total;
 #pragma unroll
@@ -521,20 +587,38 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
             }
         }
     };
+    float kept = 1.f;  // the decays of all chunks
     if (nc > 0) {
         bar();
         bar();
         own_part(0);
         bar();
         for (int c = 1; c < nc; ++c) {
-            if (odd) outputs(c - 1, std::true_type{}, std::false_type{});
-            else outputs(c - 1, std::false_type{}, std::false_type{});
+            if constexpr (OUT) {
+                if (odd) outputs(c - 1, std::true_type{}, std::false_type{});
+                else outputs(c - 1, std::false_type{}, std::false_type{});
+            } else {
+                kept *= fac[(c - 1) % 3].total;
+            }
             own_part(c);
             bar();
         }
-        if (odd) outputs(nc - 1, std::true_type{}, std::true_type{});
-        else outputs(nc - 1, std::false_type{}, std::true_type{});
+        if constexpr (OUT) {
+            if (odd) outputs(nc - 1, std::true_type{}, std::true_type{});
+            else outputs(nc - 1, std::false_type{}, std::true_type{});
+        } else {
+            kept *= fac[(nc - 1) % 3].total;
+        }
     }
+    if constexpr (!OUT) {
+#pragma unroll
+        for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(p.ws + wnext + wbase + (2 * u + e) * 256) = S[u][e];
+        if (threadIdx.x == 0 && wk.tile == 0) p.wdec[(size_t)wk.s * p.H + wk.h] = kept;
+        return;
+    }
+    if (wk.j + 1 < wk.nseg) return;
     if (!p.s_out) return;
 #pragma unroll
     for (int u = 0; u < L::UD; ++u)
@@ -548,19 +632,57 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS>::THREADS)) chunk_kernel
             }
 }
 
-template <int DK, int DVT, int DKS, int NS> hipError_t launch(ChunkParams p, hipStream_t s) {
-    typedef Lay<DK, DVT, DKS, NS> L;
+// Along each sequence: the state that segment j + 1 starts from is its own from
+// nothing (there already) plus segment j's start decayed over segment j, j >= 1.
+// Eight segments are in flight at a time.
+__global__ void __launch_bounds__(256) segment_scan_kernel(ChunkParams p, int elems) {
+    const int per = elems / 1024, part = blockIdx.x % per, pair = blockIdx.x / per;
+    const int n = pair / p.H, h = pair - n * p.H;
+    const int64_t len = seq_start(p, n + 1) - seq_start(p, n);
+    const int s0 = seg_base(p, n);
+    const int nseg = (int)min((len + p.seg - 1) / p.seg, (int64_t)(p.segs - s0));
+    if (nseg < 3 || pool_slot(p.slots, p.num_slots, n) < 0) return;
+    const size_t step = (size_t)p.H * elems;
+    f32x4 *w = reinterpret_cast<f32x4 *>(p.ws + ((size_t)s0 * p.H + h) * elems + part * 1024) + threadIdx.x;
+    const float *dec = p.wdec + (size_t)s0 * p.H + h;
+    const auto at = [&](int j) -> f32x4 & { return w[(size_t)j * (step / 4)]; };
+    f32x4 run = at(1);
+    for (int j = 2; j < nseg; j += 8) {
+        f32x4 x[8];
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j + i < nseg) {
+                x[i] = at(j + i);
+                d[i] = dec[(size_t)(j + i - 1) * p.H];
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j + i < nseg) at(j + i) = run = run * d[i] + x[i];
+    }
+}
+
+template <int DK, int DVT, int DKS, int NS, bool OUT> hipError_t launch(ChunkParams p, hipStream_t s) {
+    typedef Lay<DK, DVT, DKS, NS, OUT> L;
     p.tiles = p.dv / DVT;
-    p.units = p.N * (p.H / p.rep);
+    p.units = (p.seg ? p.segs : p.N) * (p.H / p.rep);
     const unsigned blocks = (unsigned)((p.units + 7) / 8) * 8 * p.rep * p.tiles;
-    hipLaunchKernelGGL((chunk_kernel<DK, DVT, DKS, NS>), dim3(blocks), dim3(L::THREADS), 0, s, p);
-    trace("chunk_kernel<%d, %d, %d, %d> grid=(%u) block=%d lds=%d", DK, DVT, DKS, NS, blocks, L::THREADS, L::TOTAL);
+    hipLaunchKernelGGL((chunk_kernel<DK, DVT, DKS, NS, OUT>), dim3(blocks), dim3(L::THREADS), 0, s, p);
+    trace("chunk_kernel<%d, %d, %d, %d, %d> grid=(%u) block=%d lds=%d", DK, DVT, DKS, NS, (int)OUT, blocks, L::THREADS,
+          L::TOTAL);
     return hipGetLastError();
+}
+
+// Whole states per workgroup.  (A 128 x 64 tile is split over twice the waves.)
+template <bool OUT> hipError_t launch_wide(const ChunkParams &p, int dk, hipStream_t s) {
+    constexpr int NS = OUT ? 3 : 4;
+    if (dk == 64) return p.dv == 128 ? launch<64, 128, 1, NS, OUT>(p, s) : launch<64, 64, 1, NS, OUT>(p, s);
+    return p.dv == 128 ? launch<128, 128, 1, NS, OUT>(p, s) : launch<128, 64, 2, OUT ? 2 : 4, OUT>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, hipStream_t s) {
+hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
     ChunkParams p = {};
     p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->log_decay;
     p.s_in = a->state_in; p.s_out = a->state_out; p.o = a->o; p.cu = a->cu_seqlens;
@@ -569,13 +691,24 @@ hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, hipStream_t 
     p.qs = a->q_stride; p.ks = a->k_stride; p.vs = a->v_stride;
     p.gs = (a->flags & KDA_F_DECAY_PER_HEAD) ? 0 : a->num_heads;
     p.dv = a->head_dim_v; p.state_bf16 = (a->flags & KDA_F_STATE_BF16) != 0; p.scale = a->scale;
-    const int64_t pairs = (int64_t)a->num_seqs * a->num_heads;
-    if (a->head_dim_k == 64) {
-        if (pairs * (p.dv / 64) >= 256) return p.dv == 128 ? launch<64, 128, 1, 3>(p, s) : launch<64, 64, 1, 3>(p, s);
-        return launch<64, 32, 2, 3>(p, s);
+    if (plan.tokens) {
+        const int elems = a->head_dim_k * p.dv;
+        p.seg = plan.tokens;
+        p.segs = (int)plan.segments;
+        p.ws = static_cast<float *>(a->workspace);
+        p.wdec = p.ws + (size_t)(plan.segments + 1) * p.H * elems;
+        hipError_t e = launch_wide<false>(p, a->head_dim_k, s);
+        if (e != hipSuccess) return e;
+        const unsigned blocks = (unsigned)(p.N * p.H * (elems / 1024));
+        hipLaunchKernelGGL(segment_scan_kernel, dim3(blocks), dim3(256), 0, s, p, elems);
+        trace("segment_scan_kernel grid=(%u) block=256", blocks);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        return launch_wide<true>(p, a->head_dim_k, s);
     }
-    if (pairs * (p.dv / 64) >= 256) return p.dv == 128 ? launch<128, 128, 1, 3>(p, s) : launch<128, 64, 2, 2>(p, s);
-    return launch<128, 32, 2, 3>(p, s);
+    const int64_t pairs = (int64_t)a->num_seqs * a->num_heads;
+    if (pairs * (p.dv / 64) >= 256) return launch_wide<true>(p, a->head_dim_k, s);
+    return a->head_dim_k == 64 ? launch<64, 32, 2, 3, true>(p, s) : launch<128, 32, 2, 3, true>(p, s);
 }
 
 }  // namespace kda

@@ -82,6 +82,39 @@ kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t d
     return KDA_OK;
 }
 
+// Segments of the two-pass schedule: whole chunks of 64 tokens, about one segment
+// and head for each of the 256 compute units.
+kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
+    const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
+    kda::LinattnPlan plan;
+    plan.tokens = (int)(std::max<int64_t>((T * H + 256 * 64 - 1) / (256 * 64), 1) * 64);
+    plan.segments = T / plan.tokens + N;
+    plan.bytes = ((size_t)(plan.segments + 1) * a.head_dim_k * a.head_dim_v + (size_t)plan.segments) * H * 4;
+    return plan;
+}
+
+// The automatic choice.  A lone sequence's chunks follow one another; segments
+// spread them, but read the keys and values twice.
+bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
+    const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
+    int64_t longest = (T + N - 1) / N;  // the average where lengths are not known
+    if (a.cu_seqlens_host)
+        for (int64_t n = 0; n < N; ++n)
+            longest = std::max<int64_t>(longest, (int64_t)a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n]);
+    const int64_t mean = (T * H + 255) / 256;
+    return longest >= 8 * mean && longest >= 4 * plan.tokens;
+}
+
+// Whether a call with a workspace runs two passes, and how (tokens 0: one pass).
+kda::LinattnPlan linattn_plan(const kda_linattn_prefill_args &a) {
+    const kda::LinattnPlan none{0, 0, 0};
+    if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.dtype != KDA_BF16 || a.total_tokens < 1) return none;
+    const kda::LinattnPlan plan = segment_plan(a);
+    // a launch holds fewer than 2^32 threads, up to 4096 of them for each pair
+    if ((int64_t)a.num_seqs * a.num_heads >= (int64_t)1 << 20) return none;
+    return a.schedule == KDA_SCHEDULE_TWO_PASS || prefer_segments(a, plan) ? plan : none;
+}
+
 kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) {
     kda_status st = check_linattn(a.num_seqs, a.num_heads, a.num_k_heads, a.head_dim_k, a.head_dim_v, a.dtype,
                                   a.flags, a.scale);
@@ -118,16 +151,30 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     if (a.state_out && !in_place && overlap(a.state_out, sb, a.state_in, sb))
         return fail(KDA_ERR_INVALID_ARG, "state_out partially overlaps state_in");
     const size_t gb = (size_t)H * ((a.flags & KDA_F_DECAY_PER_HEAD) ? 1 : T) * 4;
+    if (a.schedule != KDA_SCHEDULE_AUTO && a.schedule != KDA_SCHEDULE_ONE_PASS && a.schedule != KDA_SCHEDULE_TWO_PASS)
+        return fail(KDA_ERR_UNSUPPORTED, "schedule %d: automatic, one pass or two passes", a.schedule);
+    if (a.schedule == KDA_SCHEDULE_TWO_PASS) {
+        if (a.dtype != KDA_BF16) return fail(KDA_ERR_UNSUPPORTED, "the two-pass schedule needs bf16");
+        if (!a.workspace)
+            return fail(KDA_ERR_INVALID_ARG, "the two-pass schedule needs a workspace (kda_linattn_workspace_size)");
+        if (N * H >= (int64_t)1 << 20) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
+    }
+    const kda::LinattnPlan plan = a.workspace ? linattn_plan(a) : kda::LinattnPlan{0, 0, 0};
+    if (a.workspace && a.workspace_bytes < plan.bytes)
+        return fail(KDA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", a.workspace_bytes, plan.bytes);
+    if (plan.tokens && (uintptr_t)a.workspace % 16)
+        return fail(KDA_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
     const Buf bufs[] = {{a.o, rows_bytes(r[0]), "o"}, {a.state_out, sb, "state_out"},
+                        {a.workspace, plan.bytes, "workspace"},
                         {a.q, rows_bytes(r[1]), "q"}, {a.k, rows_bytes(r[2]), "k"}, {a.v, rows_bytes(r[3]), "v"},
                         {a.log_decay, gb, "log_decay"}, {a.state_in, in_place ? 0 : sb, "state_in"},
                         {a.cu_seqlens, a.cu_seqlens ? (size_t)(N + 1) * 4 : 0, "cu_seqlens"},
                         {a.state_slots, a.state_slots ? (size_t)N * 4 : 0, "state_slots"}};
-    st = check_written(bufs, 9, 2);
+    st = check_written(bufs, 10, 3);
     if (st != KDA_OK) return st;
     if (T == 0 && !a.state_out) return KDA_OK;
     if (a.scale == 0.f) a.scale = 1.0f / std::sqrt((float)a.head_dim_k);
-    hipError_t e = kda::launch_linattn_prefill(&a, stream);
+    hipError_t e = kda::launch_linattn_prefill(&a, plan, stream);
     if (e != hipSuccess) return hip_fail(e, "linattn_prefill launch");
     return KDA_OK;
 }
@@ -270,6 +317,13 @@ kda_status kda_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t st
     clear_error();
     if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     return linattn_prefill_impl(*a, stream);
+}
+
+size_t kda_linattn_workspace_size(const kda_linattn_prefill_args *a) {
+    if (!a || a->num_seqs < 1 || a->num_heads < 1 || a->total_tokens < 0 || a->total_tokens > ((int64_t)1 << 31) - 64 ||
+        a->head_dim_k < 1 || a->head_dim_v < 1 || a->head_dim_k > 128 || a->head_dim_v > 128)
+        return 0;
+    return linattn_plan(*a).bytes;
 }
 
 kda_status kda_linattn_decode(const kda_linattn_decode_args *a, hipStream_t stream) {

@@ -174,8 +174,8 @@ hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s
     return dispatch(p, a->dtype, a->flags, a->head_dim_k, s);
 }
 
-hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t s) {
-    if (a->dtype == KDA_BF16) return launch_linattn_chunks(a, s);
+hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
+    if (a->dtype == KDA_BF16) return launch_linattn_chunks(a, plan, s);
     RecurParams p = {};
     p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->log_decay;
     p.s_in = a->state_in; p.s_out = a->state_out; p.o = a->o; p.cu = a->cu_seqlens;

@@ -29,7 +29,7 @@ EXPORTS = ("kda_abi_version", "kda_set_spin_limit", "kda_status_string", "kda_la
            "kda_prefill_workspace_min_size", "kda_prefill_noalloc", "kda_decode", "kda_decode_multi",
            "kda_decode_commit", "kda_state_copy", "kda_gate_beta_proj",
            "kda_gate_beta_workspace_size", "kda_linattn_prefill", "kda_linattn_decode",
-           "kda_qk_norm_rope", "kda_gated_norm")
+           "kda_linattn_workspace_size", "kda_qk_norm_rope", "kda_gated_norm")
 MAX_SPEC_TOKENS = 8
 UPDATE_FLOATS = 6 * 128  # floats per (sequence, head, token) update record
 
@@ -123,7 +123,8 @@ class KdaLinattnPrefillArgs(ctypes.Structure):
         ("flags", _c_u32), ("scale", _c_f32),
         ("q", _p), ("k", _p), ("v", _p), ("log_decay", _p), ("state_in", _p), ("state_out", _p),
         ("o", _p), ("cu_seqlens", _p), ("cu_seqlens_host", _p), ("state_slots", _p),
-        ("num_slots", _c_i32),
+        ("num_slots", _c_i32), ("schedule", _c_i32), ("workspace", _p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -211,6 +212,8 @@ def load_library(path: str = LIB_PATH):
                         ("kda_qk_norm_rope", KdaQkNormRopeArgs), ("kda_gated_norm", KdaGatedNormArgs)):
             getattr(lib, f).restype = ctypes.c_int
             getattr(lib, f).argtypes = [ctypes.POINTER(args), _p]
+        lib.kda_linattn_workspace_size.restype = ctypes.c_size_t
+        lib.kda_linattn_workspace_size.argtypes = [ctypes.POINTER(KdaLinattnPrefillArgs)]
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -772,7 +775,8 @@ def _linattn_shapes(q, v):
 
 
 def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=None, num_seqs=None,
-                        state_in=None, state_out=None, o=None, scale=0.0, state_slots=None, stream=None):
+                        state_in=None, state_out=None, o=None, scale=0.0, state_slots=None, schedule="auto",
+                        workspace=True, stream=None):
     """Linear attention with one decay per head over packed sequences (kda_linattn_prefill):
     S <- exp(g) S + k v^T, o = scale S^T q per token.
 
@@ -782,7 +786,9 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     token.  The state is [N, H, dk, dv] fp32, or bf16 storage when those tensors are bf16;
     with state_slots (int32 [N]) the state tensors are pools and sequence n uses row
     state_slots[n].  state_out: a tensor, or True to allocate one of state_in's dtype
-    (else fp32).  scale 0 is 1 / sqrt(dk).  Returns (o [T, H, dv], state_out)."""
+    (else fp32).  scale 0 is 1 / sqrt(dk).  schedule: "auto", "one_pass" or "two_pass"
+    (include/kda.h); workspace: True allocates what the schedule needs, a uint8 tensor is
+    used, None or False gives none (one pass).  Returns (o [T, H, dv], state_out)."""
     lib = load_library()
     dev, dt = q.device, q.dtype
     T, Hk, dk, H, dv = _linattn_shapes(q, v)
@@ -811,6 +817,9 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     if o is not None:
         _need(o, "o", dt, dev)
         _shape(o, "o", (T, H, dv))
+    if torch.is_tensor(workspace):
+        _need(workspace, "workspace", torch.uint8, dev)
+    schedule = _schedule_code(schedule)
     code = _dtype_code(q)
     with _on(dev, stream):
         if o is None:
@@ -822,7 +831,12 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
         a = KdaLinattnPrefillArgs(
             N, H, Hk, dk, dv, code, T, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             log_decay.data_ptr(), _addr(state_in), _addr(state_out), o.data_ptr(), _addr(cu_seqlens), _addr(cuh),
-            slots, num_slots)
+            slots, num_slots, schedule)
+        if workspace is True:
+            need = lib.kda_linattn_workspace_size(ctypes.byref(a))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        if workspace is not None and workspace is not False:
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
         _check(lib, lib.kda_linattn_prefill(ctypes.byref(a), _stream(stream, dev)))
     return o, state_out
 

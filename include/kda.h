@@ -524,11 +524,31 @@ typedef struct {
     const int32_t *cu_seqlens_host; /* optional host copy, validated when given */
     const int32_t *state_slots;     /* [N] device pool slots, or NULL */
     int32_t num_slots;              /* pool rows when state_slots is given */
+    int32_t schedule;               /* KDA_SCHEDULE_AUTO, _ONE_PASS or _TWO_PASS */
+    void *workspace;                /* device scratch of the two-pass schedule, or NULL */
+    size_t workspace_bytes;         /* its size; see kda_linattn_workspace_size */
 } kda_linattn_prefill_args;
 
 /* Packed prompts: every sequence from its initial state to its final one.
- * Empty sequences pass their state through. */
+ * Empty sequences pass their state through.  Two schedules (results agree to
+ * rounding, and each is the same from run to run):
+ *   - one pass: a workgroup carries a (sequence, head) state, or some of its
+ *     columns, over the whole sequence; any dtype, no workspace;
+ *   - two passes (bf16): sequences are cut into segments whose states are formed
+ *     first, joined in the workspace, and then carried over them side by side:
+ *     for few (sequence, head) pairs of many tokens.
+ * KDA_SCHEDULE_AUTO takes two passes where they are the faster ones and a
+ * workspace is given.  KDA_SCHEDULE_TWO_PASS needs bf16 (else
+ * KDA_ERR_UNSUPPORTED) and a workspace; one smaller than
+ * kda_linattn_workspace_size() returns KDA_ERR_INVALID_ARG where it would be
+ * used.  The workspace is overwritten by each call and must not be shared by
+ * calls that may overlap in time. */
 kda_status kda_linattn_prefill(const kda_linattn_prefill_args *args, hipStream_t stream);
+
+/* Workspace bytes of the schedule a call runs when it is given one (0: one
+ * pass).  Depends on num_seqs, num_heads, the head dims, dtype, total_tokens,
+ * schedule and cu_seqlens_host. */
+size_t kda_linattn_workspace_size(const kda_linattn_prefill_args *args);
 
 typedef struct {
     int32_t num_seqs;        /* N >= 1: one token each */

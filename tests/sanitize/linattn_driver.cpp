@@ -12,13 +12,16 @@
 
 static int g_launch = 0;
 static kda_linattn_prefill_args g_prefill;
+static kda::LinattnPlan g_plan;
 static kda_linattn_decode_args g_decode;
 static kda_qk_norm_rope_args g_qk;
 static kda_gated_norm_args g_gated;
 static char g_msg[512];
 
 namespace kda {
-hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, hipStream_t) { ++g_launch; g_prefill = *a; return hipSuccess; }
+hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, const LinattnPlan &p, hipStream_t) {
+    ++g_launch; g_prefill = *a; g_plan = p; return hipSuccess;
+}
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t) { ++g_launch; g_decode = *a; return hipSuccess; }
 hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t) { ++g_launch; g_qk = *a; return hipSuccess; }
 hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t) { ++g_launch; g_gated = *a; return hipSuccess; }
@@ -64,16 +67,38 @@ int main() {
     p.state_out = nullptr;
     CHECK(kda_linattn_prefill(&p, nullptr) == KDA_OK && g_launch == 3);
 
+    // segments: chosen for one long sequence of few heads, never without a workspace
+    p.total_tokens = 65536; p.num_heads = p.num_k_heads = 8; p.head_dim_k = p.head_dim_v = 128;
+    p.k = addr(1); p.v = addr(2); p.q_stride = p.k_stride = p.v_stride = 0;
+    const size_t need = kda_linattn_workspace_size(&p);
+    CHECK(need > (size_t)8 * 128 * 128 * 4 * 32);
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_OK && g_launch == 4 && g_plan.tokens == 0);
+    p.workspace = addr(7); p.workspace_bytes = need - 1;
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 4);
+    p.workspace_bytes = need;
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_OK && g_launch == 5 && g_plan.tokens == 2048 && g_plan.segments == 33);
+    p.schedule = KDA_SCHEDULE_ONE_PASS;
+    CHECK(kda_linattn_workspace_size(&p) == 0);
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_OK && g_launch == 6 && g_plan.tokens == 0);
+    p.schedule = KDA_SCHEDULE_TWO_PASS; p.total_tokens = 100; p.workspace = nullptr;
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);
+    p.workspace = addr(2);
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);  // overlaps v
+    p.dtype = KDA_F32; p.workspace = addr(7);
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_UNSUPPORTED && g_launch == 6);
+    p.schedule = KDA_SCHEDULE_FUSED;
+    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_UNSUPPORTED && g_launch == 6);
+
     kda_linattn_decode_args d;
     std::memset(&d, 0, sizeof(d));
     d.num_seqs = 5; d.num_heads = 2; d.num_k_heads = 1; d.head_dim_k = 128; d.head_dim_v = 64; d.dtype = KDA_F32;
     d.flags = KDA_F_DECAY_PER_HEAD | KDA_F_STATE_BF16;
     d.q = addr(0); d.k = addr(1); d.v = addr(2); d.log_decay = (const float *)addr(3); d.state = addr(4); d.o = addr(5);
-    CHECK(kda_linattn_decode(&d, nullptr) == KDA_OK && g_launch == 4 && g_decode.k_stride == 128);
+    CHECK(kda_linattn_decode(&d, nullptr) == KDA_OK && g_launch == 7 && g_decode.k_stride == 128);
     d.state_slots = (const int32_t *)addr(6); d.num_slots = 2147483647;
     CHECK(kda_linattn_decode(&d, nullptr) == KDA_ERR_INVALID_ARG);  // a pool that size covers the other tensors
     d.num_slots = 1000;
-    CHECK(kda_linattn_decode(&d, nullptr) == KDA_OK && g_launch == 5);
+    CHECK(kda_linattn_decode(&d, nullptr) == KDA_OK && g_launch == 8);
 
     kda_qk_norm_rope_args k;
     std::memset(&k, 0, sizeof(k));
@@ -82,25 +107,25 @@ int main() {
     // in place, inside one packed projection of 512 elements a token
     k.q = k.q_out = addr(0); k.k = k.k_out = (char *)addr(0) + 256 * 2;
     k.q_stride = k.k_stride = k.q_out_stride = k.k_out_stride = 512;
-    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 6);
+    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 9);
     k.k = k.k_out = (char *)addr(0) + 248 * 2;  // shares eight elements with q
-    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);
+    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 9);
     k.k = k.k_out = (char *)addr(0) + 392 * 2;  // runs into the next token's q
-    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);
+    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 9);
     k.k = k.k_out = (char *)addr(0) + (384 + 512 * 3) * 2;  // rows three tokens on, beside every q
-    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 7);
+    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 10);
     k.k = k.k_out = nullptr; k.num_k_heads = 0; k.k_stride = k.k_out_stride = 0;
-    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 8);
+    CHECK(kda_qk_norm_rope(&k, nullptr) == KDA_OK && g_launch == 11);
 
     kda_gated_norm_args g;
     std::memset(&g, 0, sizeof(g));
     g.total_tokens = 7; g.num_heads = 3; g.head_dim = 128; g.dtype = KDA_F32; g.eps = 1e-6f;
     g.x = g.y = addr(0);
-    CHECK(kda_gated_norm(&g, nullptr) == KDA_OK && g_launch == 9 && g_gated.y_stride == 384);
+    CHECK(kda_gated_norm(&g, nullptr) == KDA_OK && g_launch == 12 && g_gated.y_stride == 384);
     g.z = (char *)addr(0) + 16;
-    CHECK(kda_gated_norm(&g, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 9);
+    CHECK(kda_gated_norm(&g, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 12);
     g.total_tokens = 0;
-    CHECK(kda_gated_norm(&g, nullptr) == KDA_OK && g_launch == 9);
+    CHECK(kda_gated_norm(&g, nullptr) == KDA_OK && g_launch == 12);
 
     if (failures) return 1;
     std::printf("linattn sanitizer run ok\n");

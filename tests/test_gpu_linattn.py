@@ -56,6 +56,37 @@ def test_prefill_many_pairs(dk, dv, dtype):
     assert torch.equal(o[keep], o1[keep]) and not torch.isfinite(o1[60:111, 3].float()).all(-1).any()
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("lengths,pool", [([700], 0), ([0, 1, 64, 65, 300, 0, 129], 9), ([5] * 130 + [400], 0)])
+def test_prefill_two_passes(dk, dv, lengths, pool):
+    """Segments of 64 tokens: one, none and many to a sequence, in place in a pool too, with
+    decays that clear the state, and a workspace that held something else."""
+    inp = make_linattn(lengths, 4, 2, dk, dv, seed=50 + len(lengths), pool=pool, device=DEV)
+    inp["log_decay"][-100, 1] = float("-inf")
+    n = len(lengths)
+    args = [inp[x] for x in ("q", "k", "v", "log_decay")]
+    ws = torch.full((1 << 27,), 255, dtype=torch.uint8, device=DEV)  # NaN everywhere
+    kw = dict(cu_seqlens=inp["cu"], state_slots=inp["slots"], schedule="two_pass", workspace=ws)
+    ref = dict(inp, state=inp["state"].clone())
+    out = inp["state"] if pool else torch.empty(n, 4, dk, dv, device=DEV)
+    o, st = kda.kda_linattn_prefill(*args, state_in=inp["state"], state_out=out, **kw)
+    rows = inp["slots"].long() if pool else torch.arange(n, device=DEV)
+    check_linattn(o, st[rows], ref, True)
+    o1, st1 = kda.kda_linattn_prefill(*args, state_in=ref["state"], state_out=torch.empty_like(out), **kw)
+    assert torch.equal(o, o1) and torch.equal(st[rows], st1[rows])
+
+
+def test_prefill_automatic_segments():
+    """A long lone sequence takes two passes by itself; the outputs agree with one pass
+    within both bounds."""
+    inp = make_linattn([6000], 2, 1, 128, 128, seed=60, device=DEV)
+    o, st = _prefill(inp)
+    o1, st1 = _prefill(inp, schedule="one_pass")
+    assert not torch.equal(o, o1)  # other roundings: the two schedules were run
+    check_linattn(o, st, inp, True)
+    check_linattn(o1, st1, inp, True)
+
+
 @pytest.mark.parametrize("H,Hk", [(1, 1), (6, 1), (6, 3), (8, 8), (33, 11)])
 @pytest.mark.parametrize("decay", ["token", "head"])
 def test_prefill_shared_key_heads_and_fixed_decays(H, Hk, decay):
