@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.hip", "kda_conv.hip", "kda_decode.hip", "kda_gate_proj.hip", "kda_linattn.hip",
-           "kda_linattn_api.hip", "kda_linattn_decode.hip", "kda_norm.hip", "kda_pool.hip",
+           "kda_linattn_api.hip", "kda_linattn_decode.hip", "kda_linattn_f32.hip", "kda_norm.hip",
+           "kda_pool.hip",
            "kda_prefill.hip", "kda_prefill_split.hip"]
 # measurement-only streaming kernels (include/kda_calib.h), a library of their own
 CALIB_LIB = os.path.join(PKG, "libkda_calib.so")
@@ -47,7 +48,7 @@ def flags():
 # Sources whose matrix-core results must stay in VGPRs (see the module docstring).
 # The one-pass prefill is left to the default heuristic: the compiler does not
 # build it with the VGPR form forced.
-VGPR_FORM = {"kda_linattn.hip", "kda_prefill_split.hip"}
+VGPR_FORM = {"kda_linattn.hip", "kda_linattn_f32.hip", "kda_prefill_split.hip"}
 
 
 def _compile(src):

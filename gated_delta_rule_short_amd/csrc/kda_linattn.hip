@@ -29,41 +29,21 @@
 // behind a token that clears the state (a large |g|).
 //
 // A future token has a zero in P, but zero times a non-finite value is not
-// zero: products never run over whole 16-token blocks of the future, and a chunk
-// whose values hold a NaN or infinity takes its diagonal blocks token by token.
+// zero: products never run over whole 16-token blocks of the future, and a NaN or
+// infinity among a chunk's values is left out of them and added on its own to the
+// rows that see it.
 #include <type_traits>
 
-#include "kda_device.h"
-#include "kda_internal.h"
+#include "kda_linattn.h"
 
 namespace kda {
 
 namespace {
 
-constexpr int C = 64;  // tokens per chunk
+constexpr int C = kFactorTokens;  // tokens per chunk
 
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((ext_vector_type(8))) unsigned short u16x8;
-
-struct ChunkParams {
-    const void *q, *k, *v;
-    const float *g;
-    const void *s_in;
-    void *s_out, *o;
-    const int32_t *cu, *slots;
-    int64_t total, qs, ks, vs, gs;  // strides in elements; gs 0: one decay per head
-    int N, H, rep, num_slots, dv, tiles, units;
-    int state_bf16;
-    float scale;
-    // segments: tokens in each (0: whole sequences), their number, the states they
-    // start from in accumulator order and their decay products, both [segment][head]
-    int seg, segs;
-    float *ws, *wdec;
-};
-
-// Workgroup barrier behind this wave's own LDS accesses.  (A fence would also
-// wait for stores and LDS DMA.)
-__device__ __forceinline__ void bar() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Piece c (16 bytes) of row r lies at piece c ^ swz(r) of its row of CPR pieces, with
 // the bits of r permuted so that no two lanes served in one cycle meet in a bank:
@@ -111,11 +91,6 @@ __device__ __forceinline__ void dma_rows(unsigned char *dst, const unsigned char
             dma16(dst + i * 1024, src + (int64_t)min(row, n - 1) * stride + (pc ^ (V ? swz_v<CPR>(row) : swz<CPR>(row))) * 16);
         }
     }
-}
-
-// First token of sequence n (n = N: the end of the last one).
-__device__ __forceinline__ int64_t seq_start(const ChunkParams &p, int n) {
-    return p.cu ? min((int64_t)max(p.cu[n], 0), p.total) : p.total / p.N * n;
 }
 
 // Segments are numbered with room for one partial one per sequence: sequence n's
@@ -242,49 +217,6 @@ __device__ __forceinline__ void stream(const Stream &m, unsigned char *lds, int 
     }
 }
 
-// Factors of one chunk: bh + bl (the decay sums, base 2), eb = 2^b, w = 2^(b_n - b)
-// (0 past the sequence), 2^(b_n) last.
-struct Factors {
-    float bh[C], bl[C], eb[C], w[C], total, pad[3];
-};
-
-// DPP move of a double, zero where a lane has no source or its row is masked off.
-template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_f64(double x) {
-    typedef __attribute__((ext_vector_type(2))) int i32x2;
-    const i32x2 v = __builtin_bit_cast(i32x2, x);
-    i32x2 r;
-    r.x = __builtin_amdgcn_update_dpp(0, v.x, CTRL, ROWS, 0xf, false);
-    r.y = __builtin_amdgcn_update_dpp(0, v.y, CTRL, ROWS, 0xf, false);
-    return __builtin_bit_cast(double, r);
-}
-__device__ __forceinline__ double lane63_f64(double x) {
-    typedef __attribute__((ext_vector_type(2))) int i32x2;
-    i32x2 v = __builtin_bit_cast(i32x2, x);
-    v.x = __builtin_amdgcn_readlane(v.x, 63);
-    v.y = __builtin_amdgcn_readlane(v.y, 63);
-    return __builtin_bit_cast(double, v);
-}
-
-__device__ __forceinline__ void chunk_factors(const float *g, Factors *f, int n, int lane) {
-    float x = g[lane];
-    x = x > 0.f ? 0.f : x;                   // NaN stays
-    x = x < -1e6f ? -1e6f : x;               // 2^(-1e6) is 0 as well; sums stay finite
-    double b = lane < n ? (double)x * 1.4426950408889634 : 0.0;
-    b += dpp_f64<0x111, 0xf>(b);  // row_shr 1, 2, 4, 8: sums inside 16 lanes
-    b += dpp_f64<0x112, 0xf>(b);
-    b += dpp_f64<0x114, 0xf>(b);
-    b += dpp_f64<0x118, 0xf>(b);
-    b += dpp_f64<0x142, 0xa>(b);  // lane 15 and 47 into the next 16
-    b += dpp_f64<0x143, 0xc>(b);  // lane 31 into the upper half
-    const double e = lane63_f64(b);
-    const float hi = (float)b;
-    f->bh[lane] = hi;
-    f->bl[lane] = (float)(b - (double)hi);
-    f->eb[lane] = exp2_fast(hi);
-    f->w[lane] = lane < n ? exp2_fast((float)(e - b)) : 0.f;
-    if (lane == 0) f->total = exp2_fast((float)e);
-}
-
 // x = a + b + c exactly, each the upper half of its word a bf16 (8 bits of x's 24).
 __device__ __forceinline__ void split3(float x, uint32_t &a, uint32_t &b, uint32_t &c) {
     a = __builtin_bit_cast(uint32_t, x);
@@ -348,17 +280,26 @@ __device__ __forceinline__ void scores(const unsigned char *lq, const unsigned c
     }
 }
 
-// acc += V^T P^T of row block rt when the values hold a non-finite one: earlier
-// blocks whole, the diagonal block token by token, added to the rows that see it.
-__device__ __forceinline__ f32x4 guarded_pv(f32x4 acc, const bf16x4 *vt, const unsigned char *pl, int rt, int lane) {
+// The finite values of x, or (BAD) the others; zeros in the place of the rest.
+template <bool BAD> __device__ __forceinline__ bf16x4 part_of(bf16x4 x) {
+    const i16x4 b = __builtin_bit_cast(i16x4, x);
+    i16x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = ((b[i] & 0x7f80) == 0x7f80) == BAD ? b[i] : (short)0;
+    return __builtin_bit_cast(bf16x4, r);
+}
+
+// What the chunk's non-finite values add to V^T P^T of row block rt: earlier blocks
+// whole, the diagonal block token by token, to the rows that see it.
+__device__ __forceinline__ f32x4 add_bad(f32x4 acc, const bf16x4 *vt, const unsigned char *pl, int rt, int lane) {
     const int r16 = lane & 15, g4 = lane >> 4;
     const bf16x4 z = {};
     for (int st = 0; st <= rt; ++st) {
         const bf16x4 pp = *reinterpret_cast<const bf16x4 *>(pl + (st >> 1) * 1024 + lane * 16 + (st & 1) * 8);
         bf16x4 vv = vt[0];
-        vv = st == 1 ? vt[1] : st == 2 ? vt[2] : st == 3 ? vt[3] : vv;
+        vv = part_of<true>(st == 1 ? vt[1] : st == 2 ? vt[2] : st == 3 ? vt[3] : vv);
         if (st < rt) {
-            acc = mma_k16w(vv, pp, acc);
+            acc = acc + mma_k16w(vv, pp, f32x4{0.f, 0.f, 0.f, 0.f});
             continue;
         }
         for (int s = 0; s < 16; ++s) {
@@ -405,7 +346,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
     if (wave >= L::NW) {  // the score waves; the first also forms the factors of chunk c + 1
         auto form = [&](int c) __attribute__((always_inline)) {
             if (c < nc)
-                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % NS) * 256), fac + c % 3,
+                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % NS) * 256)[lane], fac + c % 3,
                               min(wk.len - c * C, C), lane);
         };
         bar();
@@ -545,20 +486,21 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
     // end early).
     auto finish = [&](int c, int rt, f32x4 d, auto guarded, auto last) __attribute__((always_inline)) {
         const unsigned char *pr = lds + L::P + (c & 1) * 6144 + (rt < 2 ? rt : 2 * rt - 2) * 1024;
-        if constexpr (decltype(guarded)::value) {
-            d = guarded_pv(d, vt, pr, rt, lane);
-        } else {
-            // a half pair past the diagonal drops out on both sides
-            const bf16x4 z = {};
-            const bf16x8 p0 = *reinterpret_cast<const bf16x8 *>(pr + lane * 16);
-            const bf16x4 a0 = {p0[0], p0[1], p0[2], p0[3]}, a1 = {p0[4], p0[5], p0[6], p0[7]};
-            d = mma_k32(join8(vt[0], rt >= 1 ? vt[1] : z), join8(a0, rt >= 1 ? a1 : z), d);
-            if (rt >= 2) {
-                const bf16x8 p1 = *reinterpret_cast<const bf16x8 *>(pr + 1024 + lane * 16);
-                const bf16x4 b0 = {p1[0], p1[1], p1[2], p1[3]}, b1 = {p1[4], p1[5], p1[6], p1[7]};
-                d = mma_k32(join8(vt[2], rt >= 3 ? vt[3] : z), join8(b0, rt >= 3 ? b1 : z), d);
-            }
+        constexpr bool G = decltype(guarded)::value;  // values that are not finite come apart
+        bf16x4 vv[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) vv[t] = G ? part_of<false>(vt[t]) : vt[t];
+        // a half pair past the diagonal drops out on both sides
+        const bf16x4 z = {};
+        const bf16x8 p0 = *reinterpret_cast<const bf16x8 *>(pr + lane * 16);
+        const bf16x4 a0 = {p0[0], p0[1], p0[2], p0[3]}, a1 = {p0[4], p0[5], p0[6], p0[7]};
+        d = mma_k32(join8(vv[0], rt >= 1 ? vv[1] : z), join8(a0, rt >= 1 ? a1 : z), d);
+        if (rt >= 2) {
+            const bf16x8 p1 = *reinterpret_cast<const bf16x8 *>(pr + 1024 + lane * 16);
+            const bf16x4 b0 = {p1[0], p1[1], p1[2], p1[3]}, b1 = {p1[4], p1[5], p1[6], p1[7]};
+            d = mma_k32(join8(vv[2], rt >= 3 ? vv[3] : z), join8(b0, rt >= 3 ? b1 : z), d);
         }
+        if (G) d = add_bad(d, vt, pr, rt, lane);
         const int t = c * C + 16 * rt + r16;
         if (!decltype(last)::value || t < wk.len)
             *reinterpret_cast<bf16x4 *>(o + (size_t)t * orow) = pack4(d * p.scale);
@@ -683,14 +625,7 @@ template <bool OUT> hipError_t launch_wide(const ChunkParams &p, int dk, hipStre
 }  // namespace
 
 hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
-    ChunkParams p = {};
-    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->log_decay;
-    p.s_in = a->state_in; p.s_out = a->state_out; p.o = a->o; p.cu = a->cu_seqlens;
-    p.slots = a->state_slots; p.num_slots = a->num_slots;
-    p.total = a->total_tokens; p.N = a->num_seqs; p.H = a->num_heads; p.rep = a->num_heads / a->num_k_heads;
-    p.qs = a->q_stride; p.ks = a->k_stride; p.vs = a->v_stride;
-    p.gs = (a->flags & KDA_F_DECAY_PER_HEAD) ? 0 : a->num_heads;
-    p.dv = a->head_dim_v; p.state_bf16 = (a->flags & KDA_F_STATE_BF16) != 0; p.scale = a->scale;
+    ChunkParams p = chunk_params(a);
     if (plan.tokens) {
         const int elems = a->head_dim_k * p.dv;
         p.seg = plan.tokens;

@@ -174,7 +174,7 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     if (st != KDA_OK) return st;
     if (T == 0 && !a.state_out) return KDA_OK;
     if (a.scale == 0.f) a.scale = 1.0f / std::sqrt((float)a.head_dim_k);
-    hipError_t e = kda::launch_linattn_prefill(&a, plan, stream);
+    hipError_t e = a.dtype == KDA_BF16 ? kda::launch_linattn_chunks(&a, plan, stream) : kda::launch_linattn_f32(&a, stream);
     if (e != hipSuccess) return hip_fail(e, "linattn_prefill launch");
     return KDA_OK;
 }

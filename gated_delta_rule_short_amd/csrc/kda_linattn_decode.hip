@@ -174,17 +174,4 @@ hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s
     return dispatch(p, a->dtype, a->flags, a->head_dim_k, s);
 }
 
-hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
-    if (a->dtype == KDA_BF16) return launch_linattn_chunks(a, plan, s);
-    RecurParams p = {};
-    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->log_decay;
-    p.s_in = a->state_in; p.s_out = a->state_out; p.o = a->o; p.cu = a->cu_seqlens;
-    p.slots = a->state_slots; p.num_slots = a->num_slots;
-    p.total = a->total_tokens; p.N = a->num_seqs; p.H = a->num_heads; p.rep = a->num_heads / a->num_k_heads;
-    p.qs = a->q_stride; p.ks = a->k_stride; p.vs = a->v_stride;
-    p.gs = (a->flags & KDA_F_DECAY_PER_HEAD) ? 0 : a->num_heads;
-    p.dv = a->head_dim_v; p.scale = a->scale;
-    return dispatch(p, a->dtype, a->flags, a->head_dim_k, s);
-}
-
 }  // namespace kda

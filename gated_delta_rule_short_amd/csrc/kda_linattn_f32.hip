@@ -1,0 +1,209 @@
+// kda_linattn_f32.hip -- chunked linear attention with one decay per head for fp32
+// tokens.
+//
+// The sums are those of kda_linattn.hip over chunks of 32 tokens, on the fp32 matrix
+// instructions (no operand is rounded; at 157 TFLOP/s the chip's fp32 rate is a
+// sixteenth of its bf16 rate, so a shorter chunk with fewer products inside it pays).
+// A workgroup of four waves carries 32 columns of a (sequence, head) state: wave w
+// makes the outputs of token block w / 2 and column tile w % 2, and holds the state
+// rows of every second 16-row tile of that column tile.  The state reaches the other
+// waves, and P the outputs, through LDS in operand order; q, k, v and g of the next
+// chunk are loaded into registers while the current one is worked on.
+#include "kda_linattn.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int C = 32, DVT = 32, VP = DVT + 4;
+
+__device__ __forceinline__ bool finite4(f32x4 x) {
+    const f32x4 z = x * 0.f;  // NaN where x is not finite
+    return (z.x + z.y) + (z.z + z.w) == 0.f;
+}
+
+// x if it is finite, or (BAD) if it is not; else zero.
+template <bool BAD> __device__ __forceinline__ float part_of(float x) {
+    return (x * 0.f == 0.f) != BAD ? x : 0.f;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
+    constexpr int QP = DK + 4;          // row pitch: rows 4 apart fall on different banks
+    constexpr int QN = DK / 32;         // 16-byte pieces of a 32 x DK tensor per thread
+    constexpr int NT = DK / 16, NH = NT / 2;  // 16-row tiles of the state, and per wave
+    __shared__ __attribute__((aligned(16))) float lq[C * QP], lk[C * QP], lv[C * VP];
+    __shared__ f32x4 lp[3][64];         // P blocks (0,0), (1,0), (1,1)
+    __shared__ f32x4 ls[2][NT][64];     // the state, operand order
+    __shared__ Factors fac;
+    __shared__ int bad[4];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g4 = lane >> 4, rt = wave >> 1, ct = wave & 1;
+    const int tile = blockIdx.x % p.tiles, pair = blockIdx.x / p.tiles;
+    const int n = pair / p.H, h = pair - n * p.H;
+    const int slot = pool_slot(p.slots, p.num_slots, n);
+    if (slot < 0) return;
+    const int64_t t0 = seq_start(p, n);
+    const int len = (int)max(seq_start(p, n + 1) - t0, (int64_t)0), nc = (len + C - 1) / C;
+    const float *q = static_cast<const float *>(p.q) + t0 * p.qs + (int64_t)(h / p.rep) * DK;
+    const float *k = static_cast<const float *>(p.k) + t0 * p.ks + (int64_t)(h / p.rep) * DK;
+    const float *v = static_cast<const float *>(p.v) + t0 * p.vs + (int64_t)h * p.dv + tile * DVT;
+    const float *g = p.g + t0 * p.gs + h;
+    float *o = static_cast<float *>(p.o) + ((size_t)t0 * p.H + h) * p.dv + tile * DVT + 16 * ct + 4 * g4;
+
+    // state rows 16 (rt + 2 j) + 4 g4 + i, column r16 of tile ct
+    f32x4 S[NH];
+    const size_t sbase = (((size_t)slot * p.H + h) * DK + 16 * rt + 4 * g4) * p.dv + tile * DVT + 16 * ct + r16;
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = sbase + (size_t)(32 * j + i) * p.dv;
+            S[j][i] = !p.s_in ? 0.f
+                      : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
+                                     : static_cast<const float *>(p.s_in)[at];
+        }
+        ls[ct][rt + 2 * j][lane] = S[j];
+    }
+
+    // this thread's pieces of the next chunk (zeros past the sequence)
+    f32x4 nq[QN], nk[QN], nv;
+    float ng = 0.f;
+    const int vr = tid / 8, vc = 4 * (tid % 8);
+    auto load = [&](int c) __attribute__((always_inline)) {
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = tid + 256 * i, r = c * C + e / (DK / 4), d = 4 * (e % (DK / 4));
+            nq[i] = r < len ? *reinterpret_cast<const f32x4 *>(q + r * p.qs + d) : z;
+            nk[i] = r < len ? *reinterpret_cast<const f32x4 *>(k + r * p.ks + d) : z;
+        }
+        nv = c * C + vr < len ? *reinterpret_cast<const f32x4 *>(v + (c * C + vr) * p.vs + vc) : z;
+        if (wave == 3) ng = lane < C && c * C + lane < len ? g[(c * C + lane) * p.gs] : 0.f;
+    };
+    if (nc > 0) load(0);
+    for (int c = 0; c < nc; ++c) {
+        const int m = min(len - c * C, C);
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = tid + 256 * i, at = e / (DK / 4) * QP + 4 * (e % (DK / 4));
+            *reinterpret_cast<f32x4 *>(lq + at) = nq[i];
+            *reinterpret_cast<f32x4 *>(lk + at) = nk[i];
+        }
+        *reinterpret_cast<f32x4 *>(lv + vr * VP + vc) = nv;
+        const bool some = __any(!finite4(nv));
+        if (lane == 0) bad[wave] = some;
+        const float gc = ng;
+        bar();
+        if (c + 1 < nc) load(c + 1);
+
+        // P block of waves 0..2: row block pr, key block ps; wave 3 forms the factors
+        const int pr = wave > 0, ps = wave > 1;
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        if (wave < 3) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(lk + (16 * ps + r16) * QP + 16 * t + 4 * g4);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(lq + (16 * pr + r16) * QP + 16 * t + 4 * g4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d = mma_f32(a[i], b[i], d);
+            }
+        } else {
+            chunk_factors(gc, &fac, m, lane);
+        }
+        // S^T q of this wave's token block and column tile
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 a = ls[ct][t][lane];
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(lq + (16 * rt + r16) * QP + 16 * t + 4 * g4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc = mma_f32(a[i], b[i], acc);
+        }
+        bar();
+        acc = acc * fac.eb[16 * rt + r16];
+        if (wave < 3) {
+            const int r = 16 * pr + r16, s = 16 * ps + 4 * g4;
+            const float rh = fac.bh[r], rl = fac.bl[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = d[i] * exp2_fast((rh - fac.bh[s + i]) + (rl - fac.bl[s + i]));
+                d[i] = r >= s + i ? x : 0.f;
+            }
+            lp[wave][lane] = d;
+        }
+        // values of column r16, tokens 16 st + 4 g4 + i
+        f32x4 vt[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vt[st][i] = lv[(16 * st + 4 * g4 + i) * VP + 16 * ct + r16];
+        bar();
+        const f32x4 p1 = lp[rt][lane], p2 = lp[2][lane];  // (rt, 0), (1, 1)
+        // a value that is not finite is left out of the products, where zeros of the
+        // future would not stay zeros, and added to the rows that see it
+        const bool odd = bad[0] | bad[1] | bad[2] | bad[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = mma_f32(odd ? part_of<false>(vt[0][i]) : vt[0][i], p1[i], acc);
+        if (rt == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc = mma_f32(odd ? part_of<false>(vt[1][i]) : vt[1][i], p2[i], acc);
+        }
+        if (odd) {
+            for (int st = 0; st <= rt; ++st) {
+                const f32x4 pp = st ? p2 : p1, vv = st ? vt[1] : vt[0];
+                for (int s = 0; s < 16; ++s) {
+                    // the key slot of this token alone: lanes of group s / 4, element s % 4
+                    const int i0 = s & 3;
+                    const float x = part_of<true>(i0 == 0 ? vv[0] : i0 == 1 ? vv[1] : i0 == 2 ? vv[2] : vv[3]);
+                    const float y = i0 == 0 ? pp[0] : i0 == 1 ? pp[1] : i0 == 2 ? pp[2] : pp[3];
+                    const f32x4 e = mma_f32(g4 == s >> 2 ? x : 0.f, g4 == s >> 2 ? y : 0.f, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] += (st < rt || r16 >= s) ? e[i] : 0.f;
+                }
+            }
+        }
+        const int t = c * C + 16 * rt + r16;
+        if (t < len) *reinterpret_cast<f32x4 *>(o + (size_t)t * p.H * p.dv) = acc * p.scale;
+
+        // the state over the chunk
+        f32x4 w0 = *reinterpret_cast<const f32x4 *>(fac.w + 4 * g4) * vt[0];
+        f32x4 w1 = *reinterpret_cast<const f32x4 *>(fac.w + 16 + 4 * g4) * vt[1];
+        const float tot = fac.total;
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+            const float *kr = lk + 4 * g4 * QP + 16 * (rt + 2 * j) + r16;
+            S[j] = S[j] * tot;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[j] = mma_f32(kr[i * QP], w0[i], S[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[j] = mma_f32(kr[(16 + i) * QP], w1[i], S[j]);
+            ls[ct][rt + 2 * j][lane] = S[j];
+        }
+        bar();
+    }
+    if (!p.s_out) return;
+#pragma unroll
+    for (int j = 0; j < NH; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = sbase + (size_t)(32 * j + i) * p.dv;
+            if (p.state_bf16) static_cast<__bf16 *>(p.s_out)[at] = (__bf16)S[j][i];
+            else static_cast<float *>(p.s_out)[at] = S[j][i];
+        }
+}
+
+}  // namespace
+
+hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, hipStream_t s) {
+    ChunkParams p = chunk_params(a);
+    p.tiles = p.dv / DVT;
+    const unsigned blocks = (unsigned)p.N * p.H * p.tiles;
+    if (a->head_dim_k == 64) hipLaunchKernelGGL(chunk_f32_kernel<64>, dim3(blocks), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL(chunk_f32_kernel<128>, dim3(blocks), dim3(256), 0, s, p);
+    trace("chunk_f32_kernel<%d> grid=(%u) block=256", a->head_dim_k, blocks);
+    return hipGetLastError();
+}
+
+}  // namespace kda

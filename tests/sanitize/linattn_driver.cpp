@@ -19,9 +19,10 @@ static kda_gated_norm_args g_gated;
 static char g_msg[512];
 
 namespace kda {
-hipError_t launch_linattn_prefill(const kda_linattn_prefill_args *a, const LinattnPlan &p, hipStream_t) {
+hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &p, hipStream_t) {
     ++g_launch; g_prefill = *a; g_plan = p; return hipSuccess;
 }
+hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, hipStream_t) { ++g_launch; g_prefill = *a; return hipSuccess; }
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t) { ++g_launch; g_decode = *a; return hipSuccess; }
 hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t) { ++g_launch; g_qk = *a; return hipSuccess; }
 hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t) { ++g_launch; g_gated = *a; return hipSuccess; }
