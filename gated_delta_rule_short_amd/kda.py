@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -207,13 +208,12 @@ def load_library(path: str = LIB_PATH):
         lib.kda_gate_beta_workspace_size.argtypes = [ctypes.POINTER(KdaGateBetaArgs)]
         lib.kda_state_copy.restype = ctypes.c_int
         lib.kda_state_copy.argtypes = [ctypes.POINTER(KdaStateCopyArgs), _p]
-        for f, args in (("kda_linattn_prefill", KdaLinattnPrefillArgs),
-                        ("kda_linattn_decode", KdaLinattnDecodeArgs),
-                        ("kda_qk_norm_rope", KdaQkNormRopeArgs), ("kda_gated_norm", KdaGatedNormArgs)):
+        # arguments packed into bytes (see _PREFILL_PACK) or a structure by reference
+        for f in ("kda_linattn_prefill", "kda_linattn_decode", "kda_qk_norm_rope", "kda_gated_norm"):
             getattr(lib, f).restype = ctypes.c_int
-            getattr(lib, f).argtypes = [ctypes.POINTER(args), _p]
+            getattr(lib, f).argtypes = [_p, _p]
         lib.kda_linattn_workspace_size.restype = ctypes.c_size_t
-        lib.kda_linattn_workspace_size.argtypes = [ctypes.POINTER(KdaLinattnPrefillArgs)]
+        lib.kda_linattn_workspace_size.argtypes = [_p]
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -288,6 +288,8 @@ def _need(t, name, dtype=None, device=None):
 
 def _shape(t, name, shape):
     """Raise ValueError unless tensor `t` (if given) has exactly `shape`."""
+    if t is None or t.shape == shape:
+        return
     if t is not None and tuple(t.shape) != tuple(int(x) for x in shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(int(x) for x in shape),
                                                             tuple(t.shape)))
@@ -715,17 +717,30 @@ def gate_beta_workspace_bytes(total_tokens, num_heads):
 
 
 # ------------------------------------------------------------------ linear attention, per-head norms
-def _rows(t, name, T, heads, d, dtype, dev):
+# These calls are short (a decode step of one sequence takes a few microseconds on the
+# GPU), so their checks avoid what costs a microsecond in Python: arguments are packed
+# with struct (the layouts of the Kda*Args structures above), outputs are made with
+# empty_like, and the device and stream are switched only where they differ.
+_PREFILL_PACK = struct.Struct("@6i4qIf10PiiPN")
+_DECODE_PACK = struct.Struct("@6i3qIf7Pi4x")
+_QK_PACK = struct.Struct("@q6iIf4q8P")
+_GATED_PACK = struct.Struct("@qiiiIf4x3q4P")
+_DTYPE_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+_dense = torch.contiguous_format
+
+
+def _rows(t, name, shape, dtype, dev):
     """Token stride of a [T, heads, d] tensor whose heads are dense (0: dense tokens too)."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError("%s must have shape %s, got %s" % (name, (T, heads, d), tuple(t.shape)))
-    if t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != dev:
         raise ValueError("%s must be on %s" % (name, dev))
-    st, sh, sd = t.stride()
-    if T == 0:
+    if t.is_contiguous():
         return 0
+    T, heads, d = shape
+    st, sh, sd = t.stride()
     if sd != 1 or (heads > 1 and sh != d):
         raise ValueError("the heads of %s must be dense: strides %s" % (name, t.stride()))
     if T == 1:
@@ -735,27 +750,29 @@ def _rows(t, name, T, heads, d, dtype, dev):
     return st
 
 
-class _on:
-    """The device (and stream) a call runs on: its allocations and launches belong
-    there, whichever device and stream the caller's thread is on."""
+# The current stream of a device as an address (torch.cuda.current_stream makes an
+# object of it first, at 2 us), and the current device.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("tensors must be on a GPU, got %s" % (dev,))
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-            self.ctx = torch.cuda.stream(stream)
-        else:
-            self.ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+def _elsewhere(dev, stream):
+    """The context of a call whose device or stream is not the current one: its
+    allocations and launches belong there."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % (dev,))
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _io_code(dtype):
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s (bf16 or fp32)" % dtype)
+    return code
 
 
 def _decay(log_decay, T, H, dev):
@@ -764,14 +781,16 @@ def _decay(log_decay, T, H, dev):
     if log_decay.dim() == 1:
         _shape(log_decay, "log_decay", (H,))
         return KDA_F_DECAY_PER_HEAD
-    _shape(log_decay, "log_decay", (T, H))
+    if log_decay.shape != (T, H):
+        _shape(log_decay, "log_decay", (T, H))
     return 0
 
 
 def _linattn_shapes(q, v):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [T, Hk, dk] and v [T, H, dv], got %s and %s" % (tuple(q.shape), tuple(v.shape)))
-    return q.shape + v.shape[1:]
+    T, Hk, dk = q.shape
+    return T, Hk, dk, v.shape[1], v.shape[2]
 
 
 def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=None, num_seqs=None,
@@ -789,12 +808,13 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     (else fp32).  scale 0 is 1 / sqrt(dk).  schedule: "auto", "one_pass" or "two_pass"
     (include/kda.h); workspace: True allocates what the schedule needs, a uint8 tensor is
     used, None or False gives none (one pass).  Returns (o [T, H, dv], state_out)."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev, dt = q.device, q.dtype
     T, Hk, dk, H, dv = _linattn_shapes(q, v)
     N = (cu_seqlens.numel() - 1) if cu_seqlens is not None else int(num_seqs or 1)
-    qs, ks, vs = (_rows(q, "q", T, Hk, dk, dt, dev), _rows(k, "k", T, Hk, dk, dt, dev),
-                  _rows(v, "v", T, H, dv, dt, dev))
+    qs = _rows(q, "q", q.shape, dt, dev)
+    ks = _rows(k, "k", q.shape, dt, dev)
+    vs = _rows(v, "v", (T, H, dv), dt, dev)
     flags = _decay(log_decay, T, H, dev)
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
@@ -803,41 +823,57 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     if cu_seqlens_host is not None:
         cuh = torch.as_tensor(cu_seqlens_host, dtype=torch.int32, device="cpu").contiguous()
         _shape(cuh, "cu_seqlens_host", (N + 1,))
-    if state_slots is not None and not torch.is_tensor(state_out) and (state_out or state_in is None):
-        raise ValueError("with state_slots, pass the pool tensors as state_in / state_out")
     sdt = state_in.dtype if state_in is not None else state_out.dtype if torch.is_tensor(state_out) else torch.float32
-    for t, nm in ((state_in, "state_in"), (state_out, "state_out")):
-        if torch.is_tensor(t):
-            _need(t, nm, None, dev)
-            _pool_shape(t, nm, (H, dk, dv))
-            if t.dtype != sdt:
-                raise TypeError("state_in and state_out must have one dtype")
-            flags |= _state_flag(t)
-    slots, num_slots = _slots(state_slots, (state_in, state_out), N, dev)
+    slots = num_slots = 0
+    if state_in is not None or torch.is_tensor(state_out) or state_slots is not None:
+        if state_slots is not None and not torch.is_tensor(state_out) and (state_out or state_in is None):
+            raise ValueError("with state_slots, pass the pool tensors as state_in / state_out")
+        for t, nm in ((state_in, "state_in"), (state_out, "state_out")):
+            if torch.is_tensor(t):
+                _need(t, nm, None, dev)
+                _pool_shape(t, nm, (H, dk, dv))
+                if t.dtype != sdt:
+                    raise TypeError("state_in and state_out must have one dtype")
+                flags |= _state_flag(t)
+        _, num_slots = _slots(state_slots, (state_in, state_out), N, dev)
+        slots = state_slots.data_ptr() if state_slots is not None else 0
     if o is not None:
         _need(o, "o", dt, dev)
         _shape(o, "o", (T, H, dv))
     if torch.is_tensor(workspace):
         _need(workspace, "workspace", torch.uint8, dev)
-    schedule = _schedule_code(schedule)
-    code = _dtype_code(q)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((T, H, dv), dtype=dt, device=dev)
-        if state_out is True:
-            state_out = torch.empty((N, H, dk, dv), dtype=sdt, device=dev)
-        elif state_out is False:
-            state_out = None
-        a = KdaLinattnPrefillArgs(
+    code, sched = _io_code(dt), SCHEDULES.get(schedule)
+    if sched is None:
+        sched = _schedule_code(schedule)
+    if stream is not None or dev.index is None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return kda_linattn_prefill(
+                q, k, v, log_decay, cu_seqlens=cu_seqlens, cu_seqlens_host=cuh, num_seqs=num_seqs,
+                state_in=state_in, state_out=state_out, o=o, scale=scale, state_slots=state_slots,
+                schedule=schedule, workspace=workspace)
+    if o is None:
+        o = torch.empty_like(v, memory_format=_dense)
+    if state_out is True:
+        state_out = torch.empty((N, H, dk, dv), dtype=sdt, device=dev)
+    elif state_out is False:
+        state_out = None
+
+    def args(ws, size):
+        return _PREFILL_PACK.pack(
             N, H, Hk, dk, dv, code, T, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            log_decay.data_ptr(), _addr(state_in), _addr(state_out), o.data_ptr(), _addr(cu_seqlens), _addr(cuh),
-            slots, num_slots, schedule)
-        if workspace is True:
-            need = lib.kda_linattn_workspace_size(ctypes.byref(a))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        if workspace is not None and workspace is not False:
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        _check(lib, lib.kda_linattn_prefill(ctypes.byref(a), _stream(stream, dev)))
+            log_decay.data_ptr(), _addr(state_in) or 0, _addr(state_out) or 0, o.data_ptr(), _addr(cu_seqlens) or 0,
+            _addr(cuh) or 0, slots, num_slots, sched, ws, size)
+
+    if workspace is True:
+        need = lib.kda_linattn_workspace_size(args(0, 0))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if torch.is_tensor(workspace):
+        packed = args(workspace.data_ptr(), workspace.numel())
+    else:
+        packed = args(0, 0)
+    st = lib.kda_linattn_prefill(packed, _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
     return o, state_out
 
 
@@ -846,26 +882,34 @@ def kda_linattn_decode(q, k, v, log_decay, state, *, o=None, scale=0.0, state_sl
     (kda_linattn_decode): q, k [N, Hk, dk], v [N, H, dv], log_decay [N, H] or [H] fp32;
     state [N, H, dk, dv] (fp32, or bf16 storage), or a pool with state_slots, is updated
     in place.  Shapes, strides and types as in kda_linattn_prefill.  Returns o [N, H, dv]."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev, dt = q.device, q.dtype
     N, Hk, dk, H, dv = _linattn_shapes(q, v)
-    qs, ks, vs = (_rows(q, "q", N, Hk, dk, dt, dev), _rows(k, "k", N, Hk, dk, dt, dev),
-                  _rows(v, "v", N, H, dv, dt, dev))
+    qs = _rows(q, "q", q.shape, dt, dev)
+    ks = _rows(k, "k", q.shape, dt, dev)
+    vs = _rows(v, "v", (N, H, dv), dt, dev)
     flags = _decay(log_decay, N, H, dev) | _state_flag(state)
     _need(state, "state", None, dev)
-    _pool_shape(state, "state", (H, dk, dv))
-    slots, num_slots = _slots(state_slots, (state,), N, dev)
+    slots = num_slots = 0
+    if state_slots is not None or state.shape != (N, H, dk, dv):
+        _pool_shape(state, "state", (H, dk, dv))
+        _, num_slots = _slots(state_slots, (state,), N, dev)
+        slots = state_slots.data_ptr()
     if o is not None:
         _need(o, "o", dt, dev)
         _shape(o, "o", (N, H, dv))
-    code = _dtype_code(q)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((N, H, dv), dtype=dt, device=dev)
-        a = KdaLinattnDecodeArgs(N, H, Hk, dk, dv, code, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(),
-                                 v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), o.data_ptr(), slots,
-                                 num_slots)
-        _check(lib, lib.kda_linattn_decode(ctypes.byref(a), _stream(stream, dev)))
+    code = _io_code(dt)
+    if stream is not None or dev.index is None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return kda_linattn_decode(q, k, v, log_decay, state, o=o, scale=scale, state_slots=state_slots)
+    if o is None:
+        o = torch.empty_like(v, memory_format=_dense)
+    st = lib.kda_linattn_decode(
+        _DECODE_PACK.pack(N, H, Hk, dk, dv, code, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                          log_decay.data_ptr(), state.data_ptr(), o.data_ptr(), slots, num_slots),
+        _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
     return o
 
 
@@ -878,29 +922,33 @@ def kda_qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps
     inv_freq fp32 [R / 2] (R a multiple of 16) rotate the first R elements of each head,
     in halves, or in adjacent pairs with interleaved=True; without them nothing is
     rotated.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
-    lib = load_library()
-    dev, dt = q.device, q.dtype
+    lib = _lib or load_library()
+    dev, dt, qshape = q.device, q.dtype, q.shape
     if q.dim() != 3:
-        raise ValueError("q must be [T, Hq, D], got %s" % (tuple(q.shape),))
-    T, Hq, D = q.shape
-    qs = _rows(q, "q", T, Hq, D, dt, dev)
-    Hk = ks = qos = kos = 0
+        raise ValueError("q must be [T, Hq, D], got %s" % (tuple(qshape),))
+    T, Hq, D = qshape
+    qs = _rows(q, "q", qshape, dt, dev)
+    Hk = ks = qos = kos = R = kp = kop = wq = wk = pp = fp = 0
     if k is not None:
         if k.dim() != 3 or k.shape[1] == 0:
             raise ValueError("k must be [T, Hk, D], got %s" % (tuple(k.shape),))
         Hk = k.shape[1]
-        ks = _rows(k, "k", T, Hk, D, dt, dev)
+        ks = _rows(k, "k", (T, Hk, D), dt, dev)
+        kp = k.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
     if norm not in NORMS:
         raise ValueError("norm must be one of %s" % sorted(NORMS))
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, nm, torch.float32, dev)
-            _shape(t, nm, (D,))
-    R = 0
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.float32, dev)
+        _shape(q_weight, "q_weight", (D,))
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.float32, dev)
+        _shape(k_weight, "k_weight", (D,))
+        wk = k_weight.data_ptr()
     if positions is not None:
         _need(positions, "positions", torch.int32, dev)
         _shape(positions, "positions", (T,))
@@ -908,20 +956,29 @@ def kda_qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps
         if inv_freq.dim() != 1 or inv_freq.numel() == 0:
             raise ValueError("inv_freq must be [R / 2], got %s" % (tuple(inv_freq.shape),))
         R = 2 * inv_freq.numel()
+        pp, fp = positions.data_ptr(), inv_freq.data_ptr()
     if q_out is not None:
-        qos = _rows(q_out, "q_out", T, Hq, D, dt, dev)
+        qos = _rows(q_out, "q_out", qshape, dt, dev)
     if k_out is not None:
-        kos = _rows(k_out, "k_out", T, Hk, D, dt, dev)
-    code = _dtype_code(q)
-    with _on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
-        a = KdaQkNormRopeArgs(T, Hq, Hk, D, R, code, NORMS[norm], KDA_F_ROPE_INTERLEAVED if interleaved else 0, eps,
-                              qs, ks, qos, kos, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
-                              _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq))
-        _check(lib, lib.kda_qk_norm_rope(ctypes.byref(a), _stream(stream, dev)))
+        kos = _rows(k_out, "k_out", (T, Hk, D), dt, dev)
+    code = _io_code(dt)
+    if stream is not None or dev.index is None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return kda_qk_norm_rope(q, k, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                    positions=positions, inv_freq=inv_freq, interleaved=interleaved, q_out=q_out,
+                                    k_out=k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=_dense)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=_dense)
+        kop = k_out.data_ptr()
+    st = lib.kda_qk_norm_rope(
+        _QK_PACK.pack(T, Hq, Hk, D, R, code, NORMS[norm], KDA_F_ROPE_INTERLEAVED if interleaved else 0, eps, qs, ks,
+                      qos, kos, q.data_ptr(), kp, q_out.data_ptr(), kop, wq, wk, pp, fp),
+        _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
     return q_out, k_out
 
 
@@ -931,18 +988,20 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, y=None
     x, gate, y: [T, H, D] (bf16 or fp32, heads dense, tokens at any stride of whole 16
     bytes), D 64 or 128; gate None leaves the factor out; weight fp32 [D], [H, D] or
     None.  y may be x or gate.  Returns y."""
-    lib = load_library()
-    dev, dt = x.device, x.dtype
+    lib = _lib or load_library()
+    dev, dt, shape = x.device, x.dtype, x.shape
     if x.dim() != 3:
-        raise ValueError("x must be [T, H, D], got %s" % (tuple(x.shape),))
-    T, H, D = x.shape
-    xs = _rows(x, "x", T, H, D, dt, dev)
-    zs = ys = flags = 0
-    if act not in ("sigmoid", "silu"):
+        raise ValueError("x must be [T, H, D], got %s" % (tuple(shape),))
+    T, H, D = shape
+    xs = _rows(x, "x", shape, dt, dev)
+    zs = ys = flags = zp = wp = 0
+    if act != "sigmoid" and act != "silu":
         raise ValueError("act must be 'sigmoid' or 'silu'")
     if gate is not None:
-        zs = _rows(gate, "gate", T, H, D, dt, dev)
-        flags |= KDA_F_SILU if act == "silu" else 0
+        zs = _rows(gate, "gate", shape, dt, dev)
+        zp = gate.data_ptr()
+        if act == "silu":
+            flags = KDA_F_SILU
     if weight is not None:
         _need(weight, "weight", torch.float32, dev)
         if weight.dim() == 2:
@@ -950,15 +1009,19 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, y=None
             flags |= KDA_F_WEIGHT_PER_HEAD
         else:
             _shape(weight, "weight", (D,))
+        wp = weight.data_ptr()
     if y is not None:
-        ys = _rows(y, "y", T, H, D, dt, dev)
-    code = _dtype_code(x)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty((T, H, D), dtype=dt, device=dev)
-        a = KdaGatedNormArgs(T, H, D, code, flags, eps, xs, zs, ys, x.data_ptr(), _addr(gate), _addr(weight),
-                             y.data_ptr())
-        _check(lib, lib.kda_gated_norm(ctypes.byref(a), _stream(stream, dev)))
+        ys = _rows(y, "y", shape, dt, dev)
+    code = _io_code(dt)
+    if stream is not None or dev.index is None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return kda_gated_norm(x, gate, weight, act=act, eps=eps, y=y)
+    if y is None:
+        y = torch.empty_like(x, memory_format=_dense)
+    st = lib.kda_gated_norm(_GATED_PACK.pack(T, H, D, code, flags, eps, xs, zs, ys, x.data_ptr(), zp, wp, y.data_ptr()),
+                            _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
     return y
 
 
