@@ -33,99 +33,135 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     reinterpret_cast<f32x4 *>(p)[1] = f32x4{x[4], x[5], x[6], x[7]};
 }
 
-// Sum of squares over the D / 8 lanes of a row, in every lane of it.
-template <int D> __device__ __forceinline__ float row_sumsq(const float (&x)[8]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+// Sum over the D / 8 lanes of a row, in every lane of it.
+template <int D> __device__ __forceinline__ float row_total(float s) {
     s += KDA_DPP(s, 0xb1);   // quad_perm [1,0,3,2]
     s += KDA_DPP(s, 0x4e);   // quad_perm [2,3,0,1]
     s += KDA_DPP(s, 0x141);  // row_half_mirror
     if (D == 128) s += KDA_DPP(s, 0x140);  // row_mirror
     return s;
 }
+template <int D> __device__ __forceinline__ float row_sumsq(const float (&x)[8]) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+    return row_total<D>(s);
+}
+
+template <typename T> struct Quad;  // four neighbouring elements
+template <> struct Quad<__bf16> { typedef bf16x4 vec; };
+template <> struct Quad<float> { typedef f32x4 vec; };
+template <typename T> __device__ __forceinline__ f32x4 wide(typename Quad<T>::vec x) {
+    return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+}
+__device__ __forceinline__ void store4(__bf16 *p, f32x4 x) { *reinterpret_cast<bf16x4 *>(p) = pack4(x); }
+__device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
 
 struct QkParams {
-    const void *q, *k;
-    void *qo, *ko;
-    const float *wq, *wk, *inv_freq;
+    const void *x[2];        // q, k
+    void *y[2];
+    const float *w[2], *inv_freq;
     const int32_t *pos;
-    int64_t T, qs, ks, qos, kos;
-    int Hq, Hk, groups, per_group;  // a token's rows in `groups` runs of `per_group`
-    int R, norm, interleaved;
+    int64_t T, xs[2], ys[2];
+    int H[2], qgroups;       // heads; runs of kRun heads that q takes
+    int R, norm;
     float eps;
 };
+constexpr int kRun = 32;     // heads of one wave
 
-// One wave per (token, run of heads).  Lane i < R / 2 forms the angle of pair i:
-// the turns pos * inv_freq / 2 pi are reduced in 64 bits, so the 32-bit sine and
-// cosine see an argument below one half.  The pairs reach the lanes that need
-// them through the wave's own LDS.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(QkParams p) {
-    constexpr int LPR = D / 8, RPW = 64 / LPR;
-    __shared__ float2 cs[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t first = (int64_t)blockIdx.x * 4; first < p.T * p.groups; first += (int64_t)gridDim.x * 4) {
-    const int64_t item = first + wave;
-    const int64_t t = item / p.groups;
-    const bool live = t < p.T;
-    const int g = (int)(item - t * p.groups);
-    __syncthreads();
-    if (p.R && live && lane < p.R / 2) {
-        const double turns = (double)p.pos[t] * (double)p.inv_freq[lane] * 0.15915494309189535;
-        const float fr = (float)(turns - rint(turns));
-        float s, c;
-        sincospif(2.f * fr, &s, &c);
-        cs[wave][lane] = make_float2(c, s);
-    }
-    __syncthreads();
-    if (!live) continue;
-    const int e = lane % LPR, c0 = 8 * e, sub = lane / LPR;
-    // this lane's eight elements: pair index of each, and its partner's lane
+// One wave per (token, run of heads of q or of k).  A row's D / 8 lanes hold two quads
+// of elements each: lane e of a rotated part the quads of pairs 4 e .. 4 e + 3 (both
+// halves of the pair, whichever way they are paired), the others neighbouring quads of
+// the unrotated rest, so no element crosses lanes.  Lane i < R / 2 forms the angle of
+// pair i once for the whole run: the turns pos * inv_freq / 2 pi are reduced in 64
+// bits, so the 32-bit sine and cosine see an argument of at most one half; the pairs
+// reach the lanes that rotate by them through LDS.  4096 tokens x (64 + 64) heads x 128
+// (268 MB moved): 53 us, 5.0 TB/s, the rate of a large copy; 88 us with one quad of rows
+// in flight, pairs exchanged between lanes and cosines held for eight elements.
+template <typename T, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(64) qk_norm_rope_kernel(QkParams p) {
+    typedef typename Quad<T>::vec vec;
+    constexpr int LPR = D / 8, RPW = 64 / LPR, ITER = kRun / RPW, BATCH = ITER < 4 ? ITER : 4;
+    __shared__ float2 cs[64];
+    const int lane = threadIdx.x, e = lane % LPR, sub = lane / LPR;
     const int half = p.R / 2;
-    const bool rot = c0 < p.R;
-    float co[8], si[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int j = p.interleaved ? (c0 + i) >> 1 : (c0 < half ? c0 + i : c0 + i - half);
-        const float2 v = rot ? cs[wave][j] : make_float2(1.f, 0.f);
-        co[i] = v.x;
-        // the first of a pair takes -sin times its partner, the second +sin
-        si[i] = (p.interleaved ? (i & 1) == 0 : c0 < half) ? -v.y : v.y;
+    const bool rot = 8 * e < p.R;
+    const int at0 = rot && !INTERLEAVED ? 4 * e : 8 * e, at1 = rot && !INTERLEAVED ? half + 4 * e : 8 * e + 4;
+    const int isk = (int)blockIdx.y >= p.qgroups, h0 = (blockIdx.y - (isk ? p.qgroups : 0)) * kRun;
+    const int heads = min(p.H[isk] - h0, kRun);
+    f32x4 w0 = {1.f, 1.f, 1.f, 1.f}, w1 = w0;
+    if (p.w[isk]) {
+        w0 = *reinterpret_cast<const f32x4 *>(p.w[isk] + at0);
+        w1 = *reinterpret_cast<const f32x4 *>(p.w[isk] + at1);
     }
-    const int partner = p.interleaved || !rot ? lane : (c0 < half ? lane + half / 8 : lane - half / 8);
-    float w[2][8];
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const T *x = static_cast<const T *>(p.x[isk]) + t * p.xs[isk] + (int64_t)(h0 + sub) * D;
+        T *y = static_cast<T *>(p.y[isk]) + t * p.ys[isk] + (int64_t)(h0 + sub) * D;
+        f32x4 co = {1.f, 1.f, 1.f, 1.f}, si = {0.f, 0.f, 0.f, 0.f};
+        vec v0[BATCH], v1[BATCH];
+        auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[0][i] = p.wq ? p.wq[c0 + i] : 1.f;
-        w[1][i] = p.wk ? p.wk[c0 + i] : 1.f;
-    }
-    const int r1 = min((g + 1) * p.per_group, p.Hq + p.Hk);
-    for (int r0 = g * p.per_group; r0 < r1; r0 += RPW) {
-        const int r = r0 + sub;
-        const bool on = r < r1, isk = r >= p.Hq;
-        const int hh = isk ? r - p.Hq : r;
-        float x[8] = {};
-        if (on)
-            load8<T>((isk ? static_cast<const T *>(p.k) + t * p.ks : static_cast<const T *>(p.q) + t * p.qs) +
-                         (size_t)hh * D + c0, x);
-        if (p.norm != KDA_NORM_NONE) {
-            const float ss = row_sumsq<D>(x);
-            const float rs = p.norm == KDA_NORM_RMS ? rsqrtf(ss * (1.f / D) + p.eps) : rsqrtf(ss + p.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= rs * (isk ? w[1][i] : w[0][i]);
-        }
+            for (int i = 0; i < BATCH; ++i)
+                if ((b + i) * RPW + sub < heads) {
+                    v0[i] = *reinterpret_cast<const vec *>(x + (b + i) * RPW * D + at0);
+                    v1[i] = *reinterpret_cast<const vec *>(x + (b + i) * RPW * D + at1);
+                }
+        };
+        load(0);  // under the angles
         if (p.R) {
-            float y[8];
+            __syncthreads();
+            if (lane < half) {
+                const double turns = (double)p.pos[t] * (double)p.inv_freq[lane] * 0.15915494309189535;
+                float s, c;
+                sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+                cs[lane] = make_float2(c, s);
+            }
+            __syncthreads();
+            if (rot) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = p.interleaved ? x[i ^ 1] : __shfl(x[i], partner);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = rot ? fmaf(x[i], co[i], y[i] * si[i]) : x[i];
+                for (int i = 0; i < 4; ++i) {
+                    co[i] = cs[4 * e + i].x;
+                    si[i] = cs[4 * e + i].y;
+                }
+            }
         }
-        if (on)
-            store8((isk ? static_cast<T *>(p.ko) + t * p.kos : static_cast<T *>(p.qo) + t * p.qos) +
-                       (size_t)hh * D + c0, x);
-    }
+#pragma unroll
+        for (int b = 0; b < ITER; b += BATCH) {
+            if (b > 0) {
+                if (b * RPW >= heads) break;
+                load(b);
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const bool on = (b + i) * RPW + sub < heads;
+                f32x4 a = on ? wide<T>(v0[i]) : f32x4{}, c = on ? wide<T>(v1[i]) : f32x4{};
+                if (p.norm != KDA_NORM_NONE) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ss = fmaf(a[j], a[j], fmaf(c[j], c[j], ss));
+                    ss = row_total<D>(ss);
+                    const float rs = rsqrtf((p.norm == KDA_NORM_RMS ? ss * (1.f / D) : ss) + p.eps);
+                    a = a * (w0 * rs);
+                    c = c * (w1 * rs);
+                }
+                if (rot) {  // (never of an infinity by a zero sine in the unrotated rest)
+                    const f32x4 u = a, z = c;
+                    if (INTERLEAVED) {
+                        a = f32x4{u[0] * co[0] - u[1] * si[0], u[1] * co[0] + u[0] * si[0],
+                                  u[2] * co[1] - u[3] * si[1], u[3] * co[1] + u[2] * si[1]};
+                        c = f32x4{z[0] * co[2] - z[1] * si[2], z[1] * co[2] + z[0] * si[2],
+                                  z[2] * co[3] - z[3] * si[3], z[3] * co[3] + z[2] * si[3]};
+                    } else {
+                        a = u * co - z * si;
+                        c = z * co + u * si;
+                    }
+                }
+                if (on) {
+                    store4(y + (b + i) * RPW * D + at0, a);
+                    store4(y + (b + i) * RPW * D + at1, c);
+                }
+            }
+        }
     }
 }
 
@@ -175,30 +211,27 @@ __global__ void __launch_bounds__(256) gated_norm_kernel(GatedParams p) {
 // taken by the same ones in turn.
 constexpr int64_t kMaxBlocks = 1 << 22;
 
+template <typename T, bool INTERLEAVED> void launch_qk(const QkParams &p, int D, dim3 grid, hipStream_t s) {
+    if (D == 64) hipLaunchKernelGGL((qk_norm_rope_kernel<T, 64, INTERLEAVED>), grid, dim3(64), 0, s, p);
+    else hipLaunchKernelGGL((qk_norm_rope_kernel<T, 128, INTERLEAVED>), grid, dim3(64), 0, s, p);
+}
+
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t s) {
     QkParams p = {};
-    p.q = a->q; p.k = a->k; p.qo = a->q_out; p.ko = a->k_out;
-    p.wq = a->q_weight; p.wk = a->k_weight; p.inv_freq = a->inv_freq; p.pos = a->positions;
+    p.x[0] = a->q; p.x[1] = a->k; p.y[0] = a->q_out; p.y[1] = a->k_out;
+    p.w[0] = a->q_weight; p.w[1] = a->k_weight; p.inv_freq = a->inv_freq; p.pos = a->positions;
     p.T = a->total_tokens;
-    p.qs = a->q_stride; p.ks = a->k_stride; p.qos = a->q_out_stride; p.kos = a->k_out_stride;
-    p.Hq = a->num_q_heads; p.Hk = a->num_k_heads;
-    p.R = a->rotary_dim; p.norm = a->norm; p.interleaved = (a->flags & KDA_F_ROPE_INTERLEAVED) != 0;
-    p.eps = a->eps;
-    const int rows = p.Hq + p.Hk;
-    p.per_group = 16;
-    p.groups = (rows + p.per_group - 1) / p.per_group;
-    const int64_t items = p.T * p.groups;
-    const unsigned blocks = (unsigned)std::min<int64_t>((items + 3) / 4, kMaxBlocks);
-    if (a->dtype == KDA_BF16) {
-        if (a->head_dim == 64) hipLaunchKernelGGL((qk_norm_rope_kernel<__bf16, 64>), dim3(blocks), dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((qk_norm_rope_kernel<__bf16, 128>), dim3(blocks), dim3(256), 0, s, p);
-    } else {
-        if (a->head_dim == 64) hipLaunchKernelGGL((qk_norm_rope_kernel<float, 64>), dim3(blocks), dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((qk_norm_rope_kernel<float, 128>), dim3(blocks), dim3(256), 0, s, p);
-    }
-    trace("qk_norm_rope_kernel<D=%d> grid=(%u) block=256", a->head_dim, blocks);
+    p.xs[0] = a->q_stride; p.xs[1] = a->k_stride; p.ys[0] = a->q_out_stride; p.ys[1] = a->k_out_stride;
+    p.H[0] = a->num_q_heads; p.H[1] = a->num_k_heads;
+    p.qgroups = (p.H[0] + kRun - 1) / kRun;
+    p.R = a->rotary_dim; p.norm = a->norm; p.eps = a->eps;
+    const bool pairs = (a->flags & KDA_F_ROPE_INTERLEAVED) != 0;
+    const dim3 grid((unsigned)std::min<int64_t>(p.T, kMaxBlocks), p.qgroups + (p.H[1] + kRun - 1) / kRun);
+    if (a->dtype == KDA_BF16) pairs ? launch_qk<__bf16, true>(p, a->head_dim, grid, s) : launch_qk<__bf16, false>(p, a->head_dim, grid, s);
+    else pairs ? launch_qk<float, true>(p, a->head_dim, grid, s) : launch_qk<float, false>(p, a->head_dim, grid, s);
+    trace("qk_norm_rope_kernel<D=%d> grid=(%u, %u) block=64", a->head_dim, grid.x, grid.y);
     return hipGetLastError();
 }
 
