@@ -150,8 +150,8 @@ template <int DK, int DVT, int DKS, int NS, bool OUT> struct Lay {
     static constexpr int QB = C * DK * 2, VB = C * DVT * 2;
     static constexpr int K = OUT ? QB : 0, V = K + QB, STAGE = V + VB;  // q, k, v in a stage
     static constexpr int CPR = DK / 8, CPV = DVT / 8;     // 16-byte pieces of a row
-    static constexpr int G = NS * STAGE;                  // ring of raw decays
-    static constexpr int P = G + NS * 256;                // P of two chunks, six operand pairs of 1 KiB each
+    static constexpr int G = NS * STAGE, NG = NS < 2 ? 2 : NS;  // ring of raw decays
+    static constexpr int P = G + NG * 256;                // P of two chunks, six operand pairs of 1 KiB each
     static constexpr int B = P + (OUT ? 2 * 6144 : 0);    // decay factors of three chunks
     static constexpr int X = B + 3 * 1040;                // partial outputs of two chunks when DKS > 1
     static constexpr int XB = OUT && DKS > 1 ? NCT * 4 * DKS * 1024 : 0;
@@ -176,7 +176,7 @@ struct Stream {
 template <typename L> __device__ __forceinline__ void fetch_g(const Stream &m, unsigned char *lds, int c, int lane) {
     if (c <= m.nc)
         __builtin_amdgcn_global_load_lds(m.g + (int64_t)min(c * C + lane, m.len - 1) * m.gs,
-                                         (lds_void *)(lds + L::G + (c % L::STAGES) * 256), 4, 0, 0);
+                                         (lds_void *)(lds + L::G + (c % L::NG) * 256), 4, 0, 0);
 }
 template <typename L, int SW>
 __device__ __forceinline__ void fetch(const Stream &m, unsigned char *lds, int c, int lane) {
@@ -205,15 +205,25 @@ __device__ __forceinline__ void stream(const Stream &m, unsigned char *lds, int 
         if (c + decltype(behind)::value < m.nc) wait_vmcnt<N>();
         else wait_vmcnt<0>();
     };
-    for (int c = 0; c < NS - 1; ++c) next(c);
-    landed(0, std::integral_constant<int, NS - 2>{});
+    next(0);
+    if (SW == 0) wait_vmcnt<EACH>();
+    bar();  // g0 is there
+    for (int c = 1; c < NS - 1; ++c) next(c);
+    landed(0, std::integral_constant<int, (NS > 2 ? NS - 2 : 0)>{});
     bar();
-    next(NS - 1);
-    bar();
+    if (NS > 1) next(NS - 1);
     for (int c = 0; c < m.nc; ++c) {
-        landed(c + 1, std::integral_constant<int, NS - 2>{});
-        bar();  // c: the slot of chunk c is free, chunk c + 1 is there
-        next(c + NS);
+        if constexpr (NS == 1) {
+            bar();  // c: the slot is free
+            if (c + 1 == m.nc) break;
+            next(c + 1);
+            landed(c + 1, std::integral_constant<int, 0>{});
+            bar();
+        } else {
+            landed(c + 1, std::integral_constant<int, NS - 2>{});
+            bar();  // c: the slot of chunk c is free, chunk c + 1 is there
+            next(c + NS);
+        }
     }
 }
 
@@ -315,7 +325,7 @@ __device__ __forceinline__ f32x4 add_bad(f32x4 acc, const bf16x4 *vt, const unsi
 }
 
 template <int DK, int DVT, int DKS, int NS, bool OUT>
-__global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_kernel(ChunkParams p) {
+__global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 1 ? 4 : 1)) chunk_kernel(ChunkParams p) {
     typedef Lay<DK, DVT, DKS, NS, OUT> L;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[L::TOTAL];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -326,8 +336,9 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
     if (slot < 0) return;
     const int nc = (wk.len + C - 1) / C;
 
-    // Barriers: one when chunk 0 has landed, one when its factors are formed, then one
-    // at the end of every interval c, in which chunk c is worked on.
+    // Barriers: one when g of chunk 0 has landed, one when chunk 0 has and its factors
+    // are formed, then one at the end of every interval c, in which chunk c is worked on
+    // (and with one stage another when chunk c + 1 has landed in it).
     if (wave >= L::NW && nc == 0) return;
     if (wave >= L::NW + L::SERVE) {  // the streaming waves: they read no LDS
         const int hk = wk.h / p.rep, sw = wave - L::NW - L::SERVE;
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
     if (wave >= L::NW) {  // the score waves; the first also forms the factors of chunk c + 1
         auto form = [&](int c) __attribute__((always_inline)) {
             if (c < nc)
-                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % NS) * 256)[lane], fac + c % 3,
+                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % L::NG) * 256)[lane], fac + c % 3,
                               min(wk.len - c * C, C), lane);
         };
         bar();
@@ -362,6 +373,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
                 scores<DK, 1>(lq, lq + L::K, fac + c % 3, pl, lane);
             }
             bar();
+            if (NS == 1 && c + 1 < nc) bar();
         }
         return;
     }
@@ -383,18 +395,23 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
 #pragma unroll
             for (int e = 0; e < 2; ++e) S[u][e] = *reinterpret_cast<const f32x4 *>(p.ws + wbase + (2 * u + e) * 256);
     } else {
-        const bool given = p.s_in && wk.j == 0;
+        auto read = [&](auto *x) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < L::UD; ++u)
+            for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
-                    S[u][e][i] = !given ? 0.f
-                                 : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
-                                                : static_cast<const float *>(p.s_in)[at];
-                }
+                    for (int i = 0; i < 4; ++i)
+                        S[u][e][i] = to_f32(x[sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv]);
+        };
+        if (!p.s_in || wk.j > 0) {
+#pragma unroll
+            for (int u = 0; u < L::UD; ++u) S[u][0] = S[u][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        } else if (p.state_bf16) {
+            read(static_cast<const __bf16 *>(p.s_in));
+        } else {
+            read(static_cast<const float *>(p.s_in));
+        }
         if (!OUT && wk.j == 0) {
 #pragma unroll
             for (int u = 0; u < L::UD; ++u)
@@ -542,6 +559,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
             } else {
                 kept *= fac[(c - 1) % 3].total;
             }
+            if (NS == 1) bar();
             own_part(c);
             bar();
         }
@@ -562,16 +580,18 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS)) chunk_k
     }
     if (wk.j + 1 < wk.nseg) return;
     if (!p.s_out) return;
+    auto write = [&](auto *x) __attribute__((always_inline)) {
+        typedef typename std::remove_pointer<decltype(x)>::type E;
 #pragma unroll
-    for (int u = 0; u < L::UD; ++u)
+        for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const size_t at = sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv;
-                if (p.state_bf16) static_cast<__bf16 *>(p.s_out)[at] = (__bf16)S[u][e][i];
-                else static_cast<float *>(p.s_out)[at] = S[u][e][i];
-            }
+                for (int i = 0; i < 4; ++i)
+                    x[sbase + (size_t)(32 * u + 4 * (e ^ (g4 & 1)) + i) * p.dv] = from_f32<E>(S[u][e][i]);
+    };
+    if (p.state_bf16) write(static_cast<__bf16 *>(p.s_out));
+    else write(static_cast<float *>(p.s_out));
 }
 
 // Along each sequence: the state that segment j + 1 starts from is its own from
@@ -642,6 +662,11 @@ hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const Linatt
         return launch_wide<true>(p, a->head_dim_k, s);
     }
     const int64_t pairs = (int64_t)a->num_seqs * a->num_heads;
+    // Many short sequences: one stage and 64 columns, so that a compute unit holds two
+    // workgroups and one's loads run under the other's work.  640 workgroups (40
+    // sequences x 16 heads, dk 128, dv 64) of 64 tokens each: SHORT_FIGURES.
+    if (pairs >= 256 && p.dv == 64 && p.total <= 128 * (int64_t)p.N)
+        return a->head_dim_k == 64 ? launch<64, 64, 1, 1, true>(p, s) : launch<128, 64, 1, 1, true>(p, s);
     if (pairs * (p.dv / 64) >= 256) return launch_wide<true>(p, a->head_dim_k, s);
     return a->head_dim_k == 64 ? launch<64, 32, 2, 3, true>(p, s) : launch<128, 32, 2, 3, true>(p, s);
 }

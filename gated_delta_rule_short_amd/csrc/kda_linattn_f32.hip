@@ -9,6 +9,8 @@
 // rows of every second 16-row tile of that column tile.  The state reaches the other
 // waves, and P the outputs, through LDS in operand order; q, k, v and g of the next
 // chunk are loaded into registers while the current one is worked on.
+#include <type_traits>
+
 #include "kda_linattn.h"
 
 namespace kda {
@@ -55,17 +57,22 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     // state rows 16 (rt + 2 j) + 4 g4 + i, column r16 of tile ct
     f32x4 S[NH];
     const size_t sbase = (((size_t)slot * p.H + h) * DK + 16 * rt + 4 * g4) * p.dv + tile * DVT + 16 * ct + r16;
+    auto read = [&](auto *x) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NH; ++j) {
+        for (int j = 0; j < NH; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t at = sbase + (size_t)(32 * j + i) * p.dv;
-            S[j][i] = !p.s_in ? 0.f
-                      : p.state_bf16 ? (float)static_cast<const __bf16 *>(p.s_in)[at]
-                                     : static_cast<const float *>(p.s_in)[at];
-        }
-        ls[ct][rt + 2 * j][lane] = S[j];
+            for (int i = 0; i < 4; ++i) S[j][i] = to_f32(x[sbase + (size_t)(32 * j + i) * p.dv]);
+    };
+    if (!p.s_in) {
+#pragma unroll
+        for (int j = 0; j < NH; ++j) S[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    } else if (p.state_bf16) {
+        read(static_cast<const __bf16 *>(p.s_in));
+    } else {
+        read(static_cast<const float *>(p.s_in));
     }
+#pragma unroll
+    for (int j = 0; j < NH; ++j) ls[ct][rt + 2 * j][lane] = S[j];
 
     // this thread's pieces of the next chunk (zeros past the sequence)
     f32x4 nq[QN], nk[QN], nv;
@@ -184,14 +191,15 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         bar();
     }
     if (!p.s_out) return;
+    auto write = [&](auto *x) __attribute__((always_inline)) {
+        typedef typename std::remove_pointer<decltype(x)>::type E;
 #pragma unroll
-    for (int j = 0; j < NH; ++j)
+        for (int j = 0; j < NH; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t at = sbase + (size_t)(32 * j + i) * p.dv;
-            if (p.state_bf16) static_cast<__bf16 *>(p.s_out)[at] = (__bf16)S[j][i];
-            else static_cast<float *>(p.s_out)[at] = S[j][i];
-        }
+            for (int i = 0; i < 4; ++i) x[sbase + (size_t)(32 * j + i) * p.dv] = from_f32<E>(S[j][i]);
+    };
+    if (p.state_bf16) write(static_cast<__bf16 *>(p.s_out));
+    else write(static_cast<float *>(p.s_out));
 }
 
 }  // namespace
