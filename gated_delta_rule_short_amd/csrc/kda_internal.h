@@ -70,9 +70,8 @@ struct LinattnPlan {
     int64_t segments;  // segment numbers, and the workspace they need
     size_t bytes;
 };
-hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan,
-                                 hipStream_t s);                                  // bf16 tokens
-hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, hipStream_t s);  // fp32 tokens
+hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s);  // bf16
+hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s);     // fp32
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s);
 
 // Per-head norms: queries and keys with their rotation, and the gated output norm.

@@ -34,6 +34,16 @@ inline ChunkParams chunk_params(const kda_linattn_prefill_args *a) {
     return p;
 }
 
+// The workspace of a plan: (segments + 1) x H states, then the decay products.
+inline void use_segments(ChunkParams &p, const kda_linattn_prefill_args *a, const LinattnPlan &plan) {
+    p.seg = plan.tokens;
+    p.segs = (int)plan.segments;
+    p.ws = static_cast<float *>(a->workspace);
+    p.wdec = p.ws + (size_t)(plan.segments + 1) * p.H * a->head_dim_k * p.dv;
+}
+// Joins the segments' states along every sequence (`elems` floats each).
+hipError_t launch_segment_scan(const ChunkParams &p, int elems, hipStream_t s);
+
 // Workgroup barrier behind this wave's own LDS accesses.  (A fence would also
 // wait for stores and LDS DMA.)
 __device__ __forceinline__ void bar() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -41,6 +51,55 @@ __device__ __forceinline__ void bar() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_
 // First token of sequence n (n = N: the end of the last one).
 __device__ __forceinline__ int64_t seq_start(const ChunkParams &p, int n) {
     return p.cu ? min((int64_t)max(p.cu[n], 0), p.total) : p.total / p.N * n;
+}
+
+// Segments are numbered with room for one partial one per sequence: sequence n's
+// begin at seq_start / seg + n, and numbers past its last are unused.
+__device__ __forceinline__ int seg_base(const ChunkParams &p, int n) { return (int)(seq_start(p, n) / p.seg) + n; }
+
+// The sequence that segment number s belongs to: sixty-four probes at a time.
+__device__ __forceinline__ int seg_seq(const ChunkParams &p, int s, int lane) {
+    int lo = 0, cnt = p.N;
+    while (cnt > 1) {
+        const int step = (cnt + 63) / 64, i = lo + lane * step;
+        const bool below = i < lo + cnt && seg_base(p, i) <= s;
+        const int m = __popcll(__ballot(below));
+        lo += m > 1 ? (m - 1) * step : 0;
+        cnt = min(step, p.N - lo);
+    }
+    return lo;
+}
+
+// What a workgroup works on, from its block index: segment s (a whole sequence
+// without segments), number j of its sequence's `nseg`.  The rep * tiles workgroups
+// that read the same keys are `units` neighbours on one XCD (blocks go round the
+// eight XCDs), where they share its L2.
+struct Work {
+    int n, h, tile, s, j, nseg;
+    int64_t t0;
+    int len;
+};
+__device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) {
+    const int U = p.rep * p.tiles, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const int unit = (idx / U) * 8 + xcd, member = idx % U;
+    if (unit >= p.units) return false;
+    const int Hk = p.H / p.rep;
+    w.s = unit / Hk;
+    w.h = (unit - w.s * Hk) * p.rep + member / p.tiles;
+    w.tile = member % p.tiles;
+    w.n = p.seg ? __builtin_amdgcn_readfirstlane(seg_seq(p, w.s, lane)) : w.s;
+    w.t0 = seq_start(p, w.n);
+    w.len = (int)max(seq_start(p, w.n + 1) - w.t0, (int64_t)0);
+    w.j = 0;
+    w.nseg = 1;
+    if (p.seg) {
+        w.j = w.s - seg_base(p, w.n);
+        w.nseg = max((w.len + p.seg - 1) / p.seg, 1);
+        if (w.j >= w.nseg) return false;
+        w.t0 += (int64_t)w.j * p.seg;
+        w.len = min(w.len - w.j * p.seg, p.seg);
+    }
+    return true;
 }
 
 constexpr int kFactorTokens = 64;  // most tokens of a chunk

@@ -93,55 +93,6 @@ __device__ __forceinline__ void dma_rows(unsigned char *dst, const unsigned char
     }
 }
 
-// Segments are numbered with room for one partial one per sequence: sequence n's
-// begin at seq_start / seg + n, and numbers past its last are unused.
-__device__ __forceinline__ int seg_base(const ChunkParams &p, int n) { return (int)(seq_start(p, n) / p.seg) + n; }
-
-// The sequence that segment number s belongs to: sixty-four probes at a time.
-__device__ __forceinline__ int seg_seq(const ChunkParams &p, int s, int lane) {
-    int lo = 0, cnt = p.N;
-    while (cnt > 1) {
-        const int step = (cnt + 63) / 64, i = lo + lane * step;
-        const bool below = i < lo + cnt && seg_base(p, i) <= s;
-        const int m = __popcll(__ballot(below));
-        lo += m > 1 ? (m - 1) * step : 0;
-        cnt = min(step, p.N - lo);
-    }
-    return lo;
-}
-
-// What a workgroup works on, from its block index: segment s (a whole sequence
-// without segments), number j of its sequence's `nseg`.  The rep * tiles workgroups
-// that read the same keys are `units` neighbours on one XCD (blocks go round the
-// eight XCDs), where they share its L2.
-struct Work {
-    int n, h, tile, s, j, nseg;
-    int64_t t0;
-    int len;
-};
-__device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) {
-    const int U = p.rep * p.tiles, xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const int unit = (idx / U) * 8 + xcd, member = idx % U;
-    if (unit >= p.units) return false;
-    const int Hk = p.H / p.rep;
-    w.s = unit / Hk;
-    w.h = (unit - w.s * Hk) * p.rep + member / p.tiles;
-    w.tile = member % p.tiles;
-    w.n = p.seg ? __builtin_amdgcn_readfirstlane(seg_seq(p, w.s, lane)) : w.s;
-    w.t0 = seq_start(p, w.n);
-    w.len = (int)max(seq_start(p, w.n + 1) - w.t0, (int64_t)0);
-    w.j = 0;
-    w.nseg = 1;
-    if (p.seg) {
-        w.j = w.s - seg_base(p, w.n);
-        w.nseg = max((w.len + p.seg - 1) / p.seg, 1);
-        if (w.j >= w.nseg) return false;
-        w.t0 += (int64_t)w.j * p.seg;
-        w.len = min(w.len - w.j * p.seg, p.seg);
-    }
-    return true;
-}
-
 // LDS of a workgroup.  OUT false: the state alone, without q and P.
 template <int DK, int DVT, int DKS, int NS, bool OUT> struct Lay {
     static constexpr int NCT = DVT / 16, NW = NCT * DKS;  // column tiles, compute waves
@@ -594,6 +545,28 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
     else write(static_cast<float *>(p.s_out));
 }
 
+template <int DK, int DVT, int DKS, int NS, bool OUT> hipError_t launch(ChunkParams p, hipStream_t s) {
+    typedef Lay<DK, DVT, DKS, NS, OUT> L;
+    p.tiles = p.dv / DVT;
+    p.units = (p.seg ? p.segs : p.N) * (p.H / p.rep);
+    const unsigned blocks = (unsigned)((p.units + 7) / 8) * 8 * p.rep * p.tiles;
+    hipLaunchKernelGGL((chunk_kernel<DK, DVT, DKS, NS, OUT>), dim3(blocks), dim3(L::THREADS), 0, s, p);
+    trace("chunk_kernel<%d, %d, %d, %d, %d> grid=(%u) block=%d lds=%d", DK, DVT, DKS, NS, (int)OUT, blocks, L::THREADS,
+          L::TOTAL);
+    return hipGetLastError();
+}
+
+// Whole states per workgroup.  (A 128 x 64 tile is split over twice the waves.)
+template <bool OUT> hipError_t launch_wide(const ChunkParams &p, int dk, hipStream_t s) {
+    constexpr int NS = OUT ? 3 : 4;
+    if (dk == 64) return p.dv == 128 ? launch<64, 128, 1, NS, OUT>(p, s) : launch<64, 64, 1, NS, OUT>(p, s);
+    return p.dv == 128 ? launch<128, 128, 1, NS, OUT>(p, s) : launch<128, 64, 2, OUT ? 2 : 4, OUT>(p, s);
+}
+
+}  // namespace
+
+namespace {
+
 // Along each sequence: the state that segment j + 1 starts from is its own from
 // nothing (there already) plus segment j's start decayed over segment j, j >= 1.
 // Eight segments are in flight at a time.
@@ -624,40 +597,22 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(ChunkParams p, int el
     }
 }
 
-template <int DK, int DVT, int DKS, int NS, bool OUT> hipError_t launch(ChunkParams p, hipStream_t s) {
-    typedef Lay<DK, DVT, DKS, NS, OUT> L;
-    p.tiles = p.dv / DVT;
-    p.units = (p.seg ? p.segs : p.N) * (p.H / p.rep);
-    const unsigned blocks = (unsigned)((p.units + 7) / 8) * 8 * p.rep * p.tiles;
-    hipLaunchKernelGGL((chunk_kernel<DK, DVT, DKS, NS, OUT>), dim3(blocks), dim3(L::THREADS), 0, s, p);
-    trace("chunk_kernel<%d, %d, %d, %d, %d> grid=(%u) block=%d lds=%d", DK, DVT, DKS, NS, (int)OUT, blocks, L::THREADS,
-          L::TOTAL);
+}  // namespace
+
+hipError_t launch_segment_scan(const ChunkParams &p, int elems, hipStream_t s) {
+    const unsigned blocks = (unsigned)(p.N * p.H * (elems / 1024));
+    hipLaunchKernelGGL(segment_scan_kernel, dim3(blocks), dim3(256), 0, s, p, elems);
+    trace("segment_scan_kernel grid=(%u) block=256", blocks);
     return hipGetLastError();
 }
-
-// Whole states per workgroup.  (A 128 x 64 tile is split over twice the waves.)
-template <bool OUT> hipError_t launch_wide(const ChunkParams &p, int dk, hipStream_t s) {
-    constexpr int NS = OUT ? 3 : 4;
-    if (dk == 64) return p.dv == 128 ? launch<64, 128, 1, NS, OUT>(p, s) : launch<64, 64, 1, NS, OUT>(p, s);
-    return p.dv == 128 ? launch<128, 128, 1, NS, OUT>(p, s) : launch<128, 64, 2, OUT ? 2 : 4, OUT>(p, s);
-}
-
-}  // namespace
 
 hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
     ChunkParams p = chunk_params(a);
     if (plan.tokens) {
-        const int elems = a->head_dim_k * p.dv;
-        p.seg = plan.tokens;
-        p.segs = (int)plan.segments;
-        p.ws = static_cast<float *>(a->workspace);
-        p.wdec = p.ws + (size_t)(plan.segments + 1) * p.H * elems;
+        use_segments(p, a, plan);
         hipError_t e = launch_wide<false>(p, a->head_dim_k, s);
         if (e != hipSuccess) return e;
-        const unsigned blocks = (unsigned)(p.N * p.H * (elems / 1024));
-        hipLaunchKernelGGL(segment_scan_kernel, dim3(blocks), dim3(256), 0, s, p, elems);
-        trace("segment_scan_kernel grid=(%u) block=256", blocks);
-        e = hipGetLastError();
+        e = launch_segment_scan(p, a->head_dim_k * p.dv, s);
         if (e != hipSuccess) return e;
         return launch_wide<true>(p, a->head_dim_k, s);
     }

@@ -82,33 +82,43 @@ kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t d
     return KDA_OK;
 }
 
-// Segments of the two-pass schedule: whole chunks of 64 tokens, about one segment
-// and head for each of the 256 compute units.
+// Segments of the two-pass schedule: whole chunks of 64 tokens, one workgroup for each
+// of the 256 compute units (bf16: whole states) or two (fp32: 32 columns).
 kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
+    const int64_t groups = a.dtype == KDA_BF16 ? 256 : 512 / std::max(a.head_dim_v / 32, 1);
     kda::LinattnPlan plan;
-    plan.tokens = (int)(std::max<int64_t>((T * H + 256 * 64 - 1) / (256 * 64), 1) * 64);
+    plan.tokens = (int)(std::max<int64_t>((T * H + groups * 64 - 1) / (groups * 64), 1) * 64);
     plan.segments = T / plan.tokens + N;
     plan.bytes = ((size_t)(plan.segments + 1) * a.head_dim_k * a.head_dim_v + (size_t)plan.segments) * H * 4;
     return plan;
 }
 
-// The automatic choice.  A lone sequence's chunks follow one another; segments
-// spread them, but read the keys and values twice.
+// The automatic choice, from the times of both sides (us; dk = dv = 128; L tokens and
+// `pairs` segments x heads in two passes).  In one pass the longest sequence's chunks
+// follow one another; segments run side by side but read the keys and values twice, in
+// two more launches:
+//   bf16  one pass  5 + 1.33 longest / 64 (32-column tiles; 2.4 for whole states)
+//         two       14 + 0.045 pairs + 3.9 L / 64
+//   fp32  one pass  4 + 6.2 longest / 64;  two  18 + 11.7 L / 64
+// 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads 27/27, 47/34, 88/41,
+// 680/106; 64 heads 30/42, 52/58, 96/87, -; fp32, 8 heads 103/34, 204/47, 405/74, 3190/453.
 bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
-    const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
+    if (plan.bytes > KDA_PREFILL_WORKSPACE_CAP) return false;
+    const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads, L = plan.tokens;
     int64_t longest = (T + N - 1) / N;  // the average where lengths are not known
     if (a.cu_seqlens_host)
         for (int64_t n = 0; n < N; ++n)
             longest = std::max<int64_t>(longest, (int64_t)a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n]);
-    const int64_t mean = (T * H + 255) / 256;
-    return longest >= 8 * mean && longest >= 4 * plan.tokens;
+    if (a.dtype == KDA_F32) return 10 * longest > 19 * L + 2000;
+    const bool wide = N * H * (a.head_dim_v / 64) >= 256;
+    return (wide ? 240 : 133) * longest > 390 * L + 290 * (T / L * H) + 57600;
 }
 
 // Whether a call with a workspace runs two passes, and how (tokens 0: one pass).
 kda::LinattnPlan linattn_plan(const kda_linattn_prefill_args &a) {
     const kda::LinattnPlan none{0, 0, 0};
-    if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.dtype != KDA_BF16 || a.total_tokens < 1) return none;
+    if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.total_tokens < 1) return none;
     const kda::LinattnPlan plan = segment_plan(a);
     // a launch holds fewer than 2^32 threads, up to 4096 of them for each pair
     if ((int64_t)a.num_seqs * a.num_heads >= (int64_t)1 << 20) return none;
@@ -154,7 +164,6 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     if (a.schedule != KDA_SCHEDULE_AUTO && a.schedule != KDA_SCHEDULE_ONE_PASS && a.schedule != KDA_SCHEDULE_TWO_PASS)
         return fail(KDA_ERR_UNSUPPORTED, "schedule %d: automatic, one pass or two passes", a.schedule);
     if (a.schedule == KDA_SCHEDULE_TWO_PASS) {
-        if (a.dtype != KDA_BF16) return fail(KDA_ERR_UNSUPPORTED, "the two-pass schedule needs bf16");
         if (!a.workspace)
             return fail(KDA_ERR_INVALID_ARG, "the two-pass schedule needs a workspace (kda_linattn_workspace_size)");
         if (N * H >= (int64_t)1 << 20) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
@@ -174,7 +183,7 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     if (st != KDA_OK) return st;
     if (T == 0 && !a.state_out) return KDA_OK;
     if (a.scale == 0.f) a.scale = 1.0f / std::sqrt((float)a.head_dim_k);
-    hipError_t e = a.dtype == KDA_BF16 ? kda::launch_linattn_chunks(&a, plan, stream) : kda::launch_linattn_f32(&a, stream);
+    hipError_t e = a.dtype == KDA_BF16 ? kda::launch_linattn_chunks(&a, plan, stream) : kda::launch_linattn_f32(&a, plan, stream);
     if (e != hipSuccess) return hip_fail(e, "linattn_prefill launch");
     return KDA_OK;
 }

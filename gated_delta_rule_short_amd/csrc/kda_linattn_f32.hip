@@ -29,7 +29,8 @@ template <bool BAD> __device__ __forceinline__ float part_of(float x) {
     return (x * 0.f == 0.f) != BAD ? x : 0.f;
 }
 
-template <int DK>
+// OUT false: a segment's state alone, without q, P and outputs.
+template <int DK, bool OUT>
 __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     constexpr int QP = DK + 4;          // row pitch: rows 4 apart fall on different banks
     constexpr int QN = DK / 32;         // 16-byte pieces of a 32 x DK tensor per thread
@@ -42,12 +43,13 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4, rt = wave >> 1, ct = wave & 1;
-    const int tile = blockIdx.x % p.tiles, pair = blockIdx.x / p.tiles;
-    const int n = pair / p.H, h = pair - n * p.H;
-    const int slot = pool_slot(p.slots, p.num_slots, n);
+    Work wk;
+    if (!locate(p, wk, lane)) return;
+    if (!OUT && wk.j + 1 >= wk.nseg) return;  // nothing starts from the last segment
+    const int slot = pool_slot(p.slots, p.num_slots, wk.n);
     if (slot < 0) return;
-    const int64_t t0 = seq_start(p, n);
-    const int len = (int)max(seq_start(p, n + 1) - t0, (int64_t)0), nc = (len + C - 1) / C;
+    const int h = wk.h, tile = wk.tile, len = wk.len, nc = (len + C - 1) / C;
+    const int64_t t0 = wk.t0;
     const float *q = static_cast<const float *>(p.q) + t0 * p.qs + (int64_t)(h / p.rep) * DK;
     const float *k = static_cast<const float *>(p.k) + t0 * p.ks + (int64_t)(h / p.rep) * DK;
     const float *v = static_cast<const float *>(p.v) + t0 * p.vs + (int64_t)h * p.dv + tile * DVT;
@@ -63,7 +65,12 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j][i] = to_f32(x[sbase + (size_t)(32 * j + i) * p.dv]);
     };
-    if (!p.s_in) {
+    // where a segment starts from: see the workspace of kda_linattn.hip
+    float *ws = p.ws + ((size_t)wk.s * p.H + h) * DK * p.dv + (size_t)(tile * 4 + wave) * NH * 256 + lane * 4;
+    if (OUT && wk.nseg > 1) {
+#pragma unroll
+        for (int j = 0; j < NH; ++j) S[j] = *reinterpret_cast<const f32x4 *>(ws + j * 256);
+    } else if (!p.s_in || wk.j > 0) {
 #pragma unroll
         for (int j = 0; j < NH; ++j) S[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     } else if (p.state_bf16) {
@@ -71,8 +78,14 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     } else {
         read(static_cast<const float *>(p.s_in));
     }
+    if (!OUT && wk.j == 0) {
 #pragma unroll
-    for (int j = 0; j < NH; ++j) ls[ct][rt + 2 * j][lane] = S[j];
+        for (int j = 0; j < NH; ++j) *reinterpret_cast<f32x4 *>(ws + j * 256) = S[j];
+    }
+    if (OUT) {
+#pragma unroll
+        for (int j = 0; j < NH; ++j) ls[ct][rt + 2 * j][lane] = S[j];
+    }
 
     // this thread's pieces of the next chunk (zeros past the sequence)
     f32x4 nq[QN], nk[QN], nv;
@@ -83,19 +96,20 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
             const int e = tid + 256 * i, r = c * C + e / (DK / 4), d = 4 * (e % (DK / 4));
-            nq[i] = r < len ? *reinterpret_cast<const f32x4 *>(q + r * p.qs + d) : z;
+            if (OUT) nq[i] = r < len ? *reinterpret_cast<const f32x4 *>(q + r * p.qs + d) : z;
             nk[i] = r < len ? *reinterpret_cast<const f32x4 *>(k + r * p.ks + d) : z;
         }
         nv = c * C + vr < len ? *reinterpret_cast<const f32x4 *>(v + (c * C + vr) * p.vs + vc) : z;
         if (wave == 3) ng = lane < C && c * C + lane < len ? g[(c * C + lane) * p.gs] : 0.f;
     };
+    float kept = 1.f;  // the decays of all chunks
     if (nc > 0) load(0);
     for (int c = 0; c < nc; ++c) {
         const int m = min(len - c * C, C);
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
             const int e = tid + 256 * i, at = e / (DK / 4) * QP + 4 * (e % (DK / 4));
-            *reinterpret_cast<f32x4 *>(lq + at) = nq[i];
+            if (OUT) *reinterpret_cast<f32x4 *>(lq + at) = nq[i];
             *reinterpret_cast<f32x4 *>(lk + at) = nk[i];
         }
         *reinterpret_cast<f32x4 *>(lv + vr * VP + vc) = nv;
@@ -105,10 +119,18 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         bar();
         if (c + 1 < nc) load(c + 1);
 
+        // values of column r16, tokens 16 st + 4 g4 + i
+        f32x4 vt[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vt[st][i] = lv[(16 * st + 4 * g4 + i) * VP + 16 * ct + r16];
         // P block of waves 0..2: row block pr, key block ps; wave 3 forms the factors
         const int pr = wave > 0, ps = wave > 1;
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
-        if (wave < 3) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f}, acc = d;
+        if (wave == 3) {
+            chunk_factors(gc, &fac, m, lane);
+        } else if (OUT) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const f32x4 a = *reinterpret_cast<const f32x4 *>(lk + (16 * ps + r16) * QP + 16 * t + 4 * g4);
@@ -116,19 +138,19 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d = mma_f32(a[i], b[i], d);
             }
-        } else {
-            chunk_factors(gc, &fac, m, lane);
         }
-        // S^T q of this wave's token block and column tile
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        if (OUT) {
+            // S^T q of this wave's token block and column tile
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const f32x4 a = ls[ct][t][lane];
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(lq + (16 * rt + r16) * QP + 16 * t + 4 * g4);
+            for (int t = 0; t < NT; ++t) {
+                const f32x4 a = ls[ct][t][lane];
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(lq + (16 * rt + r16) * QP + 16 * t + 4 * g4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc = mma_f32(a[i], b[i], acc);
+                for (int i = 0; i < 4; ++i) acc = mma_f32(a[i], b[i], acc);
+            }
         }
         bar();
+        if constexpr (OUT) {
         acc = acc * fac.eb[16 * rt + r16];
         if (wave < 3) {
             const int r = 16 * pr + r16, s = 16 * ps + 4 * g4;
@@ -140,12 +162,6 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
             }
             lp[wave][lane] = d;
         }
-        // values of column r16, tokens 16 st + 4 g4 + i
-        f32x4 vt[2];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vt[st][i] = lv[(16 * st + 4 * g4 + i) * VP + 16 * ct + r16];
         bar();
         const f32x4 p1 = lp[rt][lane], p2 = lp[2][lane];  // (rt, 0), (1, 1)
         // a value that is not finite is left out of the products, where zeros of the
@@ -174,6 +190,7 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         const int t = c * C + 16 * rt + r16;
         if (t < len) *reinterpret_cast<f32x4 *>(o + (size_t)t * p.H * p.dv) = acc * p.scale;
 
+        }
         // the state over the chunk
         f32x4 w0 = *reinterpret_cast<const f32x4 *>(fac.w + 4 * g4) * vt[0];
         f32x4 w1 = *reinterpret_cast<const f32x4 *>(fac.w + 16 + 4 * g4) * vt[1];
@@ -186,10 +203,19 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
             for (int i = 0; i < 4; ++i) S[j] = mma_f32(kr[i * QP], w0[i], S[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j] = mma_f32(kr[(16 + i) * QP], w1[i], S[j]);
-            ls[ct][rt + 2 * j][lane] = S[j];
+            if (OUT) ls[ct][rt + 2 * j][lane] = S[j];
         }
+        if (!OUT) kept *= tot;
         bar();
     }
+    if constexpr (!OUT) {
+        ws += (size_t)p.H * DK * p.dv;  // what the next segment starts from
+#pragma unroll
+        for (int j = 0; j < NH; ++j) *reinterpret_cast<f32x4 *>(ws + j * 256) = S[j];
+        if (tid == 0 && tile == 0) p.wdec[(size_t)wk.s * p.H + h] = kept;
+        return;
+    }
+    if (wk.j + 1 < wk.nseg) return;
     if (!p.s_out) return;
     auto write = [&](auto *x) __attribute__((always_inline)) {
         typedef typename std::remove_pointer<decltype(x)>::type E;
@@ -202,16 +228,28 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     else write(static_cast<float *>(p.s_out));
 }
 
+template <bool OUT> hipError_t launch(const ChunkParams &p, int dk, hipStream_t s) {
+    const unsigned blocks = (unsigned)((p.units + 7) / 8) * 8 * p.rep * p.tiles;
+    if (dk == 64) hipLaunchKernelGGL((chunk_f32_kernel<64, OUT>), dim3(blocks), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((chunk_f32_kernel<128, OUT>), dim3(blocks), dim3(256), 0, s, p);
+    trace("chunk_f32_kernel<%d, %d> grid=(%u) block=256", dk, (int)OUT, blocks);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, hipStream_t s) {
+hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
     ChunkParams p = chunk_params(a);
     p.tiles = p.dv / DVT;
-    const unsigned blocks = (unsigned)p.N * p.H * p.tiles;
-    if (a->head_dim_k == 64) hipLaunchKernelGGL(chunk_f32_kernel<64>, dim3(blocks), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(chunk_f32_kernel<128>, dim3(blocks), dim3(256), 0, s, p);
-    trace("chunk_f32_kernel<%d> grid=(%u) block=256", a->head_dim_k, blocks);
-    return hipGetLastError();
+    p.units = (plan.tokens ? (int)plan.segments : p.N) * a->num_k_heads;
+    if (plan.tokens) {
+        use_segments(p, a, plan);
+        hipError_t e = launch<false>(p, a->head_dim_k, s);
+        if (e != hipSuccess) return e;
+        e = launch_segment_scan(p, a->head_dim_k * p.dv, s);
+        if (e != hipSuccess) return e;
+    }
+    return launch<true>(p, a->head_dim_k, s);
 }
 
 }  // namespace kda

@@ -533,15 +533,14 @@ typedef struct {
  * Empty sequences pass their state through.  Two schedules (results agree to
  * rounding, and each is the same from run to run):
  *   - one pass: a workgroup carries a (sequence, head) state, or some of its
- *     columns, over the whole sequence; any dtype, no workspace;
- *   - two passes (bf16): sequences are cut into segments whose states are formed
+ *     columns, over the whole sequence; no workspace;
+ *   - two passes: sequences are cut into segments whose states are formed
  *     first, joined in the workspace, and then carried over them side by side:
  *     for few (sequence, head) pairs of many tokens.
  * KDA_SCHEDULE_AUTO takes two passes where they are the faster ones and a
- * workspace is given.  KDA_SCHEDULE_TWO_PASS needs bf16 (else
- * KDA_ERR_UNSUPPORTED) and a workspace; one smaller than
- * kda_linattn_workspace_size() returns KDA_ERR_INVALID_ARG where it would be
- * used.  The workspace is overwritten by each call and must not be shared by
+ * workspace is given.  KDA_SCHEDULE_TWO_PASS needs a workspace; one smaller
+ * than kda_linattn_workspace_size() returns KDA_ERR_INVALID_ARG where it would
+ * be used.  The workspace is overwritten by each call and must not be shared by
  * calls that may overlap in time. */
 kda_status kda_linattn_prefill(const kda_linattn_prefill_args *args, hipStream_t stream);
 

@@ -22,7 +22,9 @@ namespace kda {
 hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &p, hipStream_t) {
     ++g_launch; g_prefill = *a; g_plan = p; return hipSuccess;
 }
-hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, hipStream_t) { ++g_launch; g_prefill = *a; return hipSuccess; }
+hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPlan &p, hipStream_t) {
+    ++g_launch; g_prefill = *a; g_plan = p; return hipSuccess;
+}
 hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t) { ++g_launch; g_decode = *a; return hipSuccess; }
 hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t) { ++g_launch; g_qk = *a; return hipSuccess; }
 hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t) { ++g_launch; g_gated = *a; return hipSuccess; }
@@ -85,8 +87,6 @@ int main() {
     CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);
     p.workspace = addr(2);
     CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 6);  // overlaps v
-    p.dtype = KDA_F32; p.workspace = addr(7);
-    CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_UNSUPPORTED && g_launch == 6);
     p.schedule = KDA_SCHEDULE_FUSED;
     CHECK(kda_linattn_prefill(&p, nullptr) == KDA_ERR_UNSUPPORTED && g_launch == 6);
 

@@ -58,10 +58,11 @@ def test_prefill_many_pairs(dk, dv, dtype):
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("lengths,pool", [([700], 0), ([0, 1, 64, 65, 300, 0, 129], 9), ([5] * 130 + [400], 0)])
-def test_prefill_two_passes(dk, dv, lengths, pool):
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_two_passes(dk, dv, lengths, pool, dtype):
     """Segments of 64 tokens: one, none and many to a sequence, in place in a pool too, with
     decays that clear the state, and a workspace that held something else."""
-    inp = make_linattn(lengths, 4, 2, dk, dv, seed=50 + len(lengths), pool=pool, device=DEV)
+    inp = make_linattn(lengths, 4, 2, dk, dv, dtype, seed=50 + len(lengths), pool=pool, device=DEV)
     inp["log_decay"][-100, 1] = float("-inf")
     n = len(lengths)
     args = [inp[x] for x in ("q", "k", "v", "log_decay")]
@@ -76,10 +77,11 @@ def test_prefill_two_passes(dk, dv, lengths, pool):
     assert torch.equal(o, o1) and torch.equal(st[rows], st1[rows])
 
 
-def test_prefill_automatic_segments():
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_automatic_segments(dtype):
     """A long lone sequence takes two passes by itself; the outputs agree with one pass
     within both bounds."""
-    inp = make_linattn([6000], 2, 1, 128, 128, seed=60, device=DEV)
+    inp = make_linattn([6000], 2, 1, 128, 128, dtype, seed=60, device=DEV)
     o, st = _prefill(inp)
     o1, st1 = _prefill(inp, schedule="one_pass")
     assert not torch.equal(o, o1)  # other roundings: the two schedules were run
