@@ -69,6 +69,7 @@ struct LinattnPlan {
     int tokens;        // tokens per segment, 0: whole sequences
     int64_t segments;  // segment numbers, and the workspace they need
     size_t bytes;
+    int64_t longest;   // most segments a sequence can have
 };
 hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s);  // bf16
 hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s);     // fp32

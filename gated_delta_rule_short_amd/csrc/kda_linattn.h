@@ -19,6 +19,7 @@ struct ChunkParams {
     // segments: tokens in each (0: whole sequences), their number, the states they
     // start from in accumulator order and their decay products, both [segment][head]
     int seg, segs;
+    int joined;  // a scan joins them; else every segment sums the ones before it (at most three)
     float *ws, *wdec;
 };
 
@@ -38,6 +39,7 @@ inline ChunkParams chunk_params(const kda_linattn_prefill_args *a) {
 inline void use_segments(ChunkParams &p, const kda_linattn_prefill_args *a, const LinattnPlan &plan) {
     p.seg = plan.tokens;
     p.segs = (int)plan.segments;
+    p.joined = plan.longest > 4;
     p.ws = static_cast<float *>(a->workspace);
     p.wdec = p.ws + (size_t)(plan.segments + 1) * p.H * a->head_dim_k * p.dv;
 }
@@ -95,7 +97,7 @@ __device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) 
     if (p.seg) {
         w.j = w.s - seg_base(p, w.n);
         w.nseg = max((w.len + p.seg - 1) / p.seg, 1);
-        if (w.j >= w.nseg) return false;
+        if (w.j < 0 || w.j >= w.nseg) return false;
         w.t0 += (int64_t)w.j * p.seg;
         w.len = min(w.len - w.j * p.seg, p.seg);
     }

@@ -341,10 +341,21 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
     const size_t wbase = ((size_t)wk.s * p.H + wk.h) * DK * p.dv + ((size_t)wk.tile * L::NW + wave) * L::UD * 512 + lane * 4;
     const size_t wnext = (size_t)p.H * DK * p.dv;
     if (OUT && wk.nseg > 1) {
+        // (without a scan, the segments before this one are joined here)
+        const int first = p.joined || wk.j < 2 ? 0 : wk.j - 1;  // segments back to where the sum begins
 #pragma unroll
         for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) S[u][e] = *reinterpret_cast<const f32x4 *>(p.ws + wbase + (2 * u + e) * 256);
+            for (int e = 0; e < 2; ++e)
+                S[u][e] = *reinterpret_cast<const f32x4 *>(p.ws + wbase - first * wnext + (2 * u + e) * 256);
+        for (int b = first - 1; b >= 0; --b) {
+            const float d = p.wdec[(size_t)(wk.s - b - 1) * p.H + wk.h];
+#pragma unroll
+            for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    S[u][e] = S[u][e] * d + *reinterpret_cast<const f32x4 *>(p.ws + wbase - b * wnext + (2 * u + e) * 256);
+        }
     } else {
         auto read = [&](auto *x) __attribute__((always_inline)) {
 #pragma unroll
@@ -568,39 +579,40 @@ template <bool OUT> hipError_t launch_wide(const ChunkParams &p, int dk, hipStre
 namespace {
 
 // Along each sequence: the state that segment j + 1 starts from is its own from
-// nothing (there already) plus segment j's start decayed over segment j, j >= 1.
-// Eight segments are in flight at a time.
+// nothing (there already) plus segment j's start decayed over segment j, j >= 1.  One
+// element a thread, eight segments in flight: 32 segments x 8 heads (17 MB read and
+// written): 10 us.
 __global__ void __launch_bounds__(256) segment_scan_kernel(ChunkParams p, int elems) {
-    const int per = elems / 1024, part = blockIdx.x % per, pair = blockIdx.x / per;
+    const int per = elems / 256, part = blockIdx.x % per, pair = blockIdx.x / per;
     const int n = pair / p.H, h = pair - n * p.H;
     const int64_t len = seq_start(p, n + 1) - seq_start(p, n);
     const int s0 = seg_base(p, n);
     const int nseg = (int)min((len + p.seg - 1) / p.seg, (int64_t)(p.segs - s0));
     if (nseg < 3 || pool_slot(p.slots, p.num_slots, n) < 0) return;
     const size_t step = (size_t)p.H * elems;
-    f32x4 *w = reinterpret_cast<f32x4 *>(p.ws + ((size_t)s0 * p.H + h) * elems + part * 1024) + threadIdx.x;
+    float *w = p.ws + ((size_t)s0 * p.H + h) * elems + part * 256 + threadIdx.x;
     const float *dec = p.wdec + (size_t)s0 * p.H + h;
-    const auto at = [&](int j) -> f32x4 & { return w[(size_t)j * (step / 4)]; };
-    f32x4 run = at(1);
+    float run = w[step];
     for (int j = 2; j < nseg; j += 8) {
-        f32x4 x[8];
-        float d[8];
+        float x[8], d[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j + i < nseg) {
-                x[i] = at(j + i);
-                d[i] = dec[(size_t)(j + i - 1) * p.H];
-            }
+        for (int i = 0; i < 8; ++i) {  // clamped, so that no branch stands between the loads
+            const int at = min(j + i, nseg - 1);
+            x[i] = w[(size_t)at * step];
+            d[i] = dec[(size_t)(at - 1) * p.H];
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j + i < nseg) at(j + i) = run = run * d[i] + x[i];
+        for (int i = 0; i < 8; ++i) {
+            run = fmaf(run, d[i], x[i]);
+            if (j + i < nseg) w[(size_t)(j + i) * step] = run;
+        }
     }
 }
 
 }  // namespace
 
 hipError_t launch_segment_scan(const ChunkParams &p, int elems, hipStream_t s) {
-    const unsigned blocks = (unsigned)(p.N * p.H * (elems / 1024));
+    const unsigned blocks = (unsigned)(p.N * p.H * (elems / 256));
     hipLaunchKernelGGL(segment_scan_kernel, dim3(blocks), dim3(256), 0, s, p, elems);
     trace("segment_scan_kernel grid=(%u) block=256", blocks);
     return hipGetLastError();
@@ -612,7 +624,7 @@ hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const Linatt
         use_segments(p, a, plan);
         hipError_t e = launch_wide<false>(p, a->head_dim_k, s);
         if (e != hipSuccess) return e;
-        e = launch_segment_scan(p, a->head_dim_k * p.dv, s);
+        e = p.joined ? launch_segment_scan(p, a->head_dim_k * p.dv, s) : hipSuccess;
         if (e != hipSuccess) return e;
         return launch_wide<true>(p, a->head_dim_k, s);
     }

@@ -82,15 +82,27 @@ kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t d
     return KDA_OK;
 }
 
+// Tokens of the longest sequence; `unknown` when the lengths are only on the device.
+int64_t longest_sequence(const kda_linattn_prefill_args &a, int64_t unknown) {
+    if (!a.cu_seqlens) return a.total_tokens / a.num_seqs;
+    if (!a.cu_seqlens_host) return unknown;
+    int64_t longest = 0;
+    for (int64_t n = 0; n < a.num_seqs; ++n)
+        longest = std::max<int64_t>(longest, (int64_t)a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n]);
+    return longest;
+}
+
 // Segments of the two-pass schedule: whole chunks of 64 tokens, one workgroup for each
 // of the 256 compute units (bf16: whole states) or two (fp32: 32 columns).
 kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
     const int64_t groups = a.dtype == KDA_BF16 ? 256 : 512 / std::max(a.head_dim_v / 32, 1);
     kda::LinattnPlan plan;
-    plan.tokens = (int)(std::max<int64_t>((T * H + groups * 64 - 1) / (groups * 64), 1) * 64);
+    const int64_t chunks = ((T + 63) / 64 * H + groups - 1) / groups;  // in each
+    plan.tokens = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), (int64_t)1 << 24) * 64;
     plan.segments = T / plan.tokens + N;
     plan.bytes = ((size_t)(plan.segments + 1) * a.head_dim_k * a.head_dim_v + (size_t)plan.segments) * H * 4;
+    plan.longest = (longest_sequence(a, T) + plan.tokens - 1) / plan.tokens;
     return plan;
 }
 
@@ -106,10 +118,7 @@ kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
 bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
     if (plan.bytes > KDA_PREFILL_WORKSPACE_CAP) return false;
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads, L = plan.tokens;
-    int64_t longest = (T + N - 1) / N;  // the average where lengths are not known
-    if (a.cu_seqlens_host)
-        for (int64_t n = 0; n < N; ++n)
-            longest = std::max<int64_t>(longest, (int64_t)a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n]);
+    const int64_t longest = longest_sequence(a, (T + N - 1) / N);  // the average where lengths are not known
     if (a.dtype == KDA_F32) return 10 * longest > 19 * L + 2000;
     const bool wide = N * H * (a.head_dim_v / 64) >= 256;
     return (wide ? 240 : 133) * longest > 390 * L + 290 * (T / L * H) + 57600;
@@ -117,7 +126,7 @@ bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &
 
 // Whether a call with a workspace runs two passes, and how (tokens 0: one pass).
 kda::LinattnPlan linattn_plan(const kda_linattn_prefill_args &a) {
-    const kda::LinattnPlan none{0, 0, 0};
+    const kda::LinattnPlan none{0, 0, 0, 0};
     if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.total_tokens < 1) return none;
     const kda::LinattnPlan plan = segment_plan(a);
     // a launch holds fewer than 2^32 threads, up to 4096 of them for each pair
@@ -168,7 +177,7 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
             return fail(KDA_ERR_INVALID_ARG, "the two-pass schedule needs a workspace (kda_linattn_workspace_size)");
         if (N * H >= (int64_t)1 << 20) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
     }
-    const kda::LinattnPlan plan = a.workspace ? linattn_plan(a) : kda::LinattnPlan{0, 0, 0};
+    const kda::LinattnPlan plan = a.workspace ? linattn_plan(a) : kda::LinattnPlan{0, 0, 0, 0};
     if (a.workspace && a.workspace_bytes < plan.bytes)
         return fail(KDA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", a.workspace_bytes, plan.bytes);
     if (plan.tokens && (uintptr_t)a.workspace % 16)

@@ -67,9 +67,16 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     };
     // where a segment starts from: see the workspace of kda_linattn.hip
     float *ws = p.ws + ((size_t)wk.s * p.H + h) * DK * p.dv + (size_t)(tile * 4 + wave) * NH * 256 + lane * 4;
+    const size_t next = (size_t)p.H * DK * p.dv;
     if (OUT && wk.nseg > 1) {
+        const int first = p.joined || wk.j < 2 ? 0 : wk.j - 1;
 #pragma unroll
-        for (int j = 0; j < NH; ++j) S[j] = *reinterpret_cast<const f32x4 *>(ws + j * 256);
+        for (int j = 0; j < NH; ++j) S[j] = *reinterpret_cast<const f32x4 *>(ws - first * next + j * 256);
+        for (int b = first - 1; b >= 0; --b) {
+            const float x = p.wdec[(size_t)(wk.s - b - 1) * p.H + h];
+#pragma unroll
+            for (int j = 0; j < NH; ++j) S[j] = S[j] * x + *reinterpret_cast<const f32x4 *>(ws - b * next + j * 256);
+        }
     } else if (!p.s_in || wk.j > 0) {
 #pragma unroll
         for (int j = 0; j < NH; ++j) S[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         bar();
     }
     if constexpr (!OUT) {
-        ws += (size_t)p.H * DK * p.dv;  // what the next segment starts from
+        ws += next;  // what the next segment starts from
 #pragma unroll
         for (int j = 0; j < NH; ++j) *reinterpret_cast<f32x4 *>(ws + j * 256) = S[j];
         if (tid == 0 && tile == 0) p.wdec[(size_t)wk.s * p.H + h] = kept;
@@ -246,7 +253,7 @@ hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPl
         use_segments(p, a, plan);
         hipError_t e = launch<false>(p, a->head_dim_k, s);
         if (e != hipSuccess) return e;
-        e = launch_segment_scan(p, a->head_dim_k * p.dv, s);
+        e = p.joined ? launch_segment_scan(p, a->head_dim_k * p.dv, s) : hipSuccess;
         if (e != hipSuccess) return e;
     }
     return launch<true>(p, a->head_dim_k, s);

@@ -816,27 +816,42 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     ks = _rows(k, "k", q.shape, dt, dev)
     vs = _rows(v, "v", (T, H, dv), dt, dev)
     flags = _decay(log_decay, T, H, dev)
+    cup = 0
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         _shape(cu_seqlens, "cu_seqlens", (N + 1,))
-    cuh = None
-    if cu_seqlens_host is not None:
-        cuh = torch.as_tensor(cu_seqlens_host, dtype=torch.int32, device="cpu").contiguous()
+        cup = cu_seqlens.data_ptr()
+    cuh = cu_seqlens_host
+    if cuh is not None:
+        if not (torch.is_tensor(cuh) and cuh.dtype is torch.int32 and cuh.is_cpu and cuh.is_contiguous()):
+            cuh = torch.as_tensor(cuh, dtype=torch.int32, device="cpu").contiguous()
         _shape(cuh, "cu_seqlens_host", (N + 1,))
-    sdt = state_in.dtype if state_in is not None else state_out.dtype if torch.is_tensor(state_out) else torch.float32
-    slots = num_slots = 0
-    if state_in is not None or torch.is_tensor(state_out) or state_slots is not None:
-        if state_slots is not None and not torch.is_tensor(state_out) and (state_out or state_in is None):
+    given = torch.is_tensor(state_out)
+    sdt = state_in.dtype if state_in is not None else state_out.dtype if given else torch.float32
+    slots = num_slots = sip = sop = 0
+    if state_slots is not None:
+        if not given and (state_out or state_in is None):
             raise ValueError("with state_slots, pass the pool tensors as state_in / state_out")
         for t, nm in ((state_in, "state_in"), (state_out, "state_out")):
-            if torch.is_tensor(t):
-                _need(t, nm, None, dev)
-                _pool_shape(t, nm, (H, dk, dv))
-                if t.dtype != sdt:
-                    raise TypeError("state_in and state_out must have one dtype")
-                flags |= _state_flag(t)
+            _pool_shape(t, nm, (H, dk, dv))
         _, num_slots = _slots(state_slots, (state_in, state_out), N, dev)
-        slots = state_slots.data_ptr() if state_slots is not None else 0
+        slots = state_slots.data_ptr()
+    shape = (N, H, dk, dv)
+    if state_in is not None:
+        _need(state_in, "state_in", None, dev)
+        if slots == 0 and state_in.shape != shape:
+            _pool_shape(state_in, "state_in", (H, dk, dv))
+            _slots(None, (state_in,), N, dev)
+        flags |= _state_flag(state_in)
+        sip = state_in.data_ptr()
+    if given:
+        _need(state_out, "state_out", None, dev)
+        if slots == 0 and state_out.shape != shape:
+            _pool_shape(state_out, "state_out", (H, dk, dv))
+            _slots(None, (state_out,), N, dev)
+        if state_out.dtype is not sdt:
+            raise TypeError("state_in and state_out must have one dtype")
+        flags |= _state_flag(state_out)
     if o is not None:
         _need(o, "o", dt, dev)
         _shape(o, "o", (T, H, dv))
@@ -854,15 +869,16 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     if o is None:
         o = torch.empty_like(v, memory_format=_dense)
     if state_out is True:
-        state_out = torch.empty((N, H, dk, dv), dtype=sdt, device=dev)
+        state_out = torch.empty(shape, dtype=sdt, device=dev)
     elif state_out is False:
         state_out = None
+    if state_out is not None:
+        sop = state_out.data_ptr()
 
     def args(ws, size):
         return _PREFILL_PACK.pack(
             N, H, Hk, dk, dv, code, T, qs, ks, vs, flags, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            log_decay.data_ptr(), _addr(state_in) or 0, _addr(state_out) or 0, o.data_ptr(), _addr(cu_seqlens) or 0,
-            _addr(cuh) or 0, slots, num_slots, sched, ws, size)
+            log_decay.data_ptr(), sip, sop, o.data_ptr(), cup, 0 if cuh is None else cuh.data_ptr(), slots, num_slots, sched, ws, size)
 
     if workspace is True:
         need = lib.kda_linattn_workspace_size(args(0, 0))

@@ -546,7 +546,7 @@ kda_status kda_linattn_prefill(const kda_linattn_prefill_args *args, hipStream_t
 
 /* Workspace bytes of the schedule a call runs when it is given one (0: one
  * pass).  Depends on num_seqs, num_heads, the head dims, dtype, total_tokens,
- * schedule and cu_seqlens_host. */
+ * schedule, cu_seqlens_host and whether cu_seqlens is given. */
 size_t kda_linattn_workspace_size(const kda_linattn_prefill_args *args);
 
 typedef struct {

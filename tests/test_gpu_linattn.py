@@ -57,7 +57,8 @@ def test_prefill_many_pairs(dk, dv, dtype):
 
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
-@pytest.mark.parametrize("lengths,pool", [([700], 0), ([0, 1, 64, 65, 300, 0, 129], 9), ([5] * 130 + [400], 0)])
+@pytest.mark.parametrize("lengths,pool", [([700], 0), ([0, 1, 64, 65, 300, 0, 129], 9), ([5] * 130 + [400], 0),
+                                          ([250, 200, 64, 1], 6)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_prefill_two_passes(dk, dv, lengths, pool, dtype):
     """Segments of 64 tokens: one, none and many to a sequence, in place in a pool too, with

@@ -133,6 +133,21 @@ def test_gated_norm_refusals(lib, kw, status):
     assert lib.kda_last_error() != b""
 
 
+def test_workspace_size(lib):
+    def size(**kw):
+        return lib.kda_linattn_workspace_size(ctypes.byref(_prefill(cu_seqlens=None, num_seqs=1, **kw)))
+    assert lib.kda_linattn_workspace_size(None) == 0
+    assert size(total_tokens=0) == 0 and size(total_tokens=-5) == 0 and size(total_tokens=1 << 31) == 0
+    assert size(total_tokens=128) == 0                      # one pass is the faster one
+    assert size(total_tokens=128, schedule=2) > 0           # asked for
+    assert size(total_tokens=1 << 20) > 0 and size(total_tokens=1 << 20, schedule=1) == 0
+    assert size(total_tokens=1 << 20, schedule=2, num_heads=1 << 21, num_k_heads=1) == 0  # too many pairs
+    for T in (1, 63, 64, 65, (1 << 31) - 64):               # sizes far beyond any memory stay arithmetic
+        for H in (1, 7, 1 << 19):
+            for dtype in (0, 1):
+                size(total_tokens=T, schedule=2, num_heads=H, num_k_heads=1, dtype=dtype)
+
+
 def test_null_arguments(lib):
     for f in ("kda_linattn_prefill", "kda_linattn_decode", "kda_qk_norm_rope", "kda_gated_norm"):
         assert getattr(lib, f)(None, None) == INV
