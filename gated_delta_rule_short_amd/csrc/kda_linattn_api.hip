@@ -63,6 +63,13 @@ kda_status check_rows_written(const Rows *r, int n, int n_written, const int *sa
     return KDA_OK;
 }
 
+// (Sequence, head) pairs of a grid, which holds a multiple of eight key heads.
+int64_t grid_pairs(int64_t N, int32_t H, int32_t Hk) { return (N * Hk + 7) / 8 * 8 * (H / Hk); }
+
+// Pairs of the two-pass schedule: its scan takes 16,384 threads for each, and a launch
+// holds fewer than 2^32.
+constexpr int64_t kMaxSegmentPairs = (int64_t)1 << 18;
+
 kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv, kda_dtype dt, uint32_t flags,
                          float scale) {
     if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs = %d, must be >= 1", N);
@@ -77,7 +84,7 @@ kda_status check_linattn(int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t d
     if (!std::isfinite(scale) || scale < 0.f)
         return fail(KDA_ERR_INVALID_ARG, "scale must be finite and >= 0 (0 = default)");
     // a launch holds fewer than 2^32 threads, up to 1024 of them for each pair
-    if ((int64_t)N * H >= (int64_t)1 << 22)
+    if (grid_pairs(N, H, Hk) >= (int64_t)1 << 22)
         return fail(KDA_ERR_INVALID_ARG, "num_seqs * num_heads too large");
     return KDA_OK;
 }
@@ -128,9 +135,8 @@ bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &
 kda::LinattnPlan linattn_plan(const kda_linattn_prefill_args &a) {
     const kda::LinattnPlan none{0, 0, 0, 0};
     if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.total_tokens < 1) return none;
+    if ((int64_t)a.num_seqs * a.num_heads >= kMaxSegmentPairs) return none;
     const kda::LinattnPlan plan = segment_plan(a);
-    // a launch holds fewer than 2^32 threads, up to 4096 of them for each pair
-    if ((int64_t)a.num_seqs * a.num_heads >= (int64_t)1 << 20) return none;
     return a.schedule == KDA_SCHEDULE_TWO_PASS || prefer_segments(a, plan) ? plan : none;
 }
 
@@ -175,7 +181,7 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     if (a.schedule == KDA_SCHEDULE_TWO_PASS) {
         if (!a.workspace)
             return fail(KDA_ERR_INVALID_ARG, "the two-pass schedule needs a workspace (kda_linattn_workspace_size)");
-        if (N * H >= (int64_t)1 << 20) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
+        if (N * H >= kMaxSegmentPairs) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
     }
     const kda::LinattnPlan plan = a.workspace ? linattn_plan(a) : kda::LinattnPlan{0, 0, 0, 0};
     if (a.workspace && a.workspace_bytes < plan.bytes)

@@ -148,6 +148,19 @@ def test_workspace_size(lib):
                 size(total_tokens=T, schedule=2, num_heads=H, num_k_heads=1, dtype=dtype)
 
 
+def test_grids_beyond_a_launch_are_refused(lib):
+    # blocks of eight key heads: one key head takes the room of eight
+    assert lib.kda_linattn_prefill(ctypes.byref(_prefill(num_seqs=1, num_heads=1 << 19, num_k_heads=1)), None) == INV
+    ws = dict(workspace=_addr(12), workspace_bytes=1 << 50, schedule=2)
+    for N, H in ((1, 1 << 18), (1 << 16, 4)):               # the scan's threads
+        a = _prefill(num_seqs=N, num_heads=H, num_k_heads=H, cu_seqlens=None, total_tokens=N * 512, head_dim_k=64,
+                     state_in=None, state_out=None, q=_addr(1 << 10), k=_addr(1 << 12), v=_addr(1 << 14),
+                     o=_addr(1 << 16), log_decay=_addr(1 << 18), **ws)
+        assert lib.kda_linattn_prefill(ctypes.byref(a), None) == INV
+        assert b"pairs" in lib.kda_last_error()
+        assert lib.kda_linattn_workspace_size(ctypes.byref(a)) == 0
+
+
 def test_null_arguments(lib):
     for f in ("kda_linattn_prefill", "kda_linattn_decode", "kda_qk_norm_rope", "kda_gated_norm"):
         assert getattr(lib, f)(None, None) == INV
