@@ -107,7 +107,8 @@ __device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) 
 constexpr int kFactorTokens = 64;  // most tokens of a chunk
 
 // Factors of one chunk: bh + bl (the decay sums, base 2), eb = 2^b, w = 2^(b_n - b)
-// (0 past the sequence), 2^(b_n) last.
+// (0 past the sequence), 2^(b_n) last; w and the last also over `after`, the sum of
+// the chunks behind it.
 struct Factors {
     float bh[kFactorTokens], bl[kFactorTokens], eb[kFactorTokens], w[kFactorTokens], total, pad[3];
 };
@@ -129,8 +130,9 @@ __device__ __forceinline__ double lane63_f64(double x) {
     return __builtin_bit_cast(double, v);
 }
 
-// x: the log-decay of token `lane` of the chunk (ignored past its n tokens).
-__device__ __forceinline__ void chunk_factors(float x, Factors *f, int n, int lane) {
+// x: the log-decay of token `lane` of the chunk (ignored past its n tokens).  Returns
+// the chunk's sum.
+__device__ __forceinline__ double chunk_factors(float x, Factors *f, int n, int lane, double after = 0.0) {
     x = x > 0.f ? 0.f : x;                   // NaN stays
     x = x < -1e6f ? -1e6f : x;               // 2^(-1e6) is 0 as well; sums stay finite
     double b = lane < n ? (double)x * 1.4426950408889634 : 0.0;
@@ -145,8 +147,9 @@ __device__ __forceinline__ void chunk_factors(float x, Factors *f, int n, int la
     f->bh[lane] = hi;
     f->bl[lane] = (float)(b - (double)hi);
     f->eb[lane] = exp2_fast(hi);
-    f->w[lane] = lane < n ? exp2_fast((float)(e - b)) : 0.f;
-    if (lane == 0) f->total = exp2_fast((float)e);
+    f->w[lane] = lane < n ? exp2_fast((float)(e - b + after)) : 0.f;
+    if (lane == 0) f->total = exp2_fast((float)(e + after));
+    return e;
 }
 
 }  // namespace kda

@@ -19,7 +19,10 @@
 // launches spread them over the GPU: every segment's state from nothing (the same
 // kernel without q, P and outputs), a scan of those states along each sequence, and
 // the outputs with every segment starting from its scanned state.  The keys and
-// values are read twice for it.
+// values are read twice for it, first from the last chunk to the first: what the
+// outputs begin with was read last and is still cached (1 x 65,536 tokens x 8 heads
+// 202 -> 195 us, 1 x 4096 x 64 95 -> 91 us; and the state needs no decay on the way).
+// Segments of up to four to a sequence are joined by the third launch itself.
 //
 // Rounding: P and the state under q are rounded to bf16 once as operands (the
 // outputs are bf16 themselves).  The decayed values of the state's own product
@@ -122,19 +125,20 @@ struct Stream {
     int64_t xs, vs, gs;
     int len, nc;
 };
-// (One past the last chunk is fetched too, from its last token, so that every chunk
-// comes with the same number of loads.)
+// (One past the last chunk is fetched too, from tokens that are there, so that every
+// chunk comes with the same number of loads.)  Without q the chunks come last to first
+// and are whole ones.
 template <typename L> __device__ __forceinline__ void fetch_g(const Stream &m, unsigned char *lds, int c, int lane) {
-    if (c <= m.nc)
-        __builtin_amdgcn_global_load_lds(m.g + (int64_t)min(c * C + lane, m.len - 1) * m.gs,
-                                         (lds_void *)(lds + L::G + (c % L::NG) * 256), 4, 0, 0);
+    if (c > m.nc) return;
+    const int t = L::Q ? min(c * C + lane, m.len - 1) : max(m.nc - 1 - c, 0) * C + lane;
+    __builtin_amdgcn_global_load_lds(m.g + (int64_t)t * m.gs, (lds_void *)(lds + L::G + (c % L::NG) * 256), 4, 0, 0);
 }
 template <typename L, int SW>
 __device__ __forceinline__ void fetch(const Stream &m, unsigned char *lds, int c, int lane) {
     if (c >= m.nc) return;
     unsigned char *st = lds + (c % L::STAGES) * L::STAGE;
-    const int n = min(m.len - c * C, C);
-    const int64_t t = (int64_t)c * C;
+    const int n = L::Q ? min(m.len - c * C, C) : C;
+    const int64_t t = (int64_t)(L::Q ? c : m.nc - 1 - c) * C;
     if constexpr (L::Q) dma_rows<L::CPR, false>(st + SW * L::K, m.x + t * m.xs, m.xs, n, lane);
     else dma_rows<L::CPR, false, SW * L::CPR / 2, (SW + 1) * L::CPR / 2>(st, m.x + t * m.xs, m.xs, n, lane);
     dma_rows<L::CPV, true, SW * L::CPV / 2, (SW + 1) * L::CPV / 2>(st + L::V, m.v + t * m.vs, m.vs, n, lane);
@@ -306,10 +310,12 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
     }
     Factors *fac = reinterpret_cast<Factors *>(lds + L::B);
     if (wave >= L::NW) {  // the score waves; the first also forms the factors of chunk c + 1
+        double after = 0.0;  // the decays of the chunks behind (already worked on without q)
         auto form = [&](int c) __attribute__((always_inline)) {
-            if (c < nc)
-                chunk_factors(reinterpret_cast<const float *>(lds + L::G + (c % L::NG) * 256)[lane], fac + c % 3,
-                              min(wk.len - c * C, C), lane);
+            if (c >= nc) return;
+            const float x = reinterpret_cast<const float *>(lds + L::G + (c % L::NG) * 256)[lane];
+            const double e = chunk_factors(x, fac + c % 3, OUT ? min(wk.len - c * C, C) : C, lane, after);
+            if (!OUT) after += e;
         };
         bar();
         if (wave == L::NW) form(0);
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
     const int r16 = lane & 15, g4 = lane >> 4;
     const int ct = wave % L::NCT, hh = wave / L::NCT;
     const int col = wk.tile * DVT + 16 * ct;
+    // Without q, S begins at zero and the start is added behind the last chunk.
     // S[u][e][i]: row 32 (hh UD + u) + 8 g4 + 4 (e ^ g4 % 2) + i, column col + r16 (the
     // exchanged halves keep the transposed reads of k off each other's banks)
     f32x4 S[L::UD][2];
@@ -420,11 +427,13 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
         odd = __any(has_non_finite(join8(vt[0], vt[1]), join8(vt[2], vt[3])));
         }
         // the state over the chunk: K^T V' with V' in three exact parts
-        const float tot = f->total;
+        if constexpr (OUT) {
+            const float tot = f->total;
 #pragma unroll
-        for (int u = 0; u < L::UD; ++u)
+            for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) S[u][e] = S[u][e] * tot;
+                for (int e = 0; e < 2; ++e) S[u][e] = S[u][e] * tot;
+        }
 #pragma unroll
         for (int kp = 0; kp < 2; ++kp) {
             bf16x8 v3[3];
@@ -508,7 +517,16 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
             }
         }
     };
-    float kept = 1.f;  // the decays of all chunks
+    f32x4 start[L::UD][2];
+    if constexpr (!OUT) {
+#pragma unroll
+        for (int u = 0; u < L::UD; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                start[u][e] = S[u][e];
+                S[u][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+    }
     if (nc > 0) {
         bar();
         bar();
@@ -518,8 +536,6 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
             if constexpr (OUT) {
                 if (odd) outputs(c - 1, std::true_type{}, std::false_type{});
                 else outputs(c - 1, std::false_type{}, std::false_type{});
-            } else {
-                kept *= fac[(c - 1) % 3].total;
             }
             if (NS == 1) bar();
             own_part(c);
@@ -528,15 +544,15 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
         if constexpr (OUT) {
             if (odd) outputs(nc - 1, std::true_type{}, std::true_type{});
             else outputs(nc - 1, std::false_type{}, std::true_type{});
-        } else {
-            kept *= fac[(nc - 1) % 3].total;
         }
     }
     if constexpr (!OUT) {
+        const float kept = fac[(nc - 1) % 3].total;  // the decays of all chunks
 #pragma unroll
         for (int u = 0; u < L::UD; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(p.ws + wnext + wbase + (2 * u + e) * 256) = S[u][e];
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<f32x4 *>(p.ws + wnext + wbase + (2 * u + e) * 256) = S[u][e] + start[u][e] * kept;
         if (threadIdx.x == 0 && wk.tile == 0) p.wdec[(size_t)wk.s * p.H + wk.h] = kept;
         return;
     }
