@@ -65,6 +65,12 @@ hipError_t launch_prefill_fused(const kda_prefill_args *a, hipStream_t s);
 
 // Linear attention with one decay per head; strides and scale are resolved.  The
 // plan cuts the sequences into segments that share the workspace.
+// Up to this many segments of a sequence are joined by the launch that makes the
+// outputs, every one summing those before it; more by a launch of their own.  One
+// sequence of 16 segments x 16 heads 33 -> 26 us, four of 8 x 8 48 -> 38, one of 16 x 1
+// 19 -> 23; at 32 the sums cost as much as the launch.
+constexpr int kJoinSegments = 16;
+
 struct LinattnPlan {
     int tokens;        // tokens per segment, 0: whole sequences
     int64_t segments;  // segment numbers, and the workspace they need

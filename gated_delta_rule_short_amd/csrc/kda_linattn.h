@@ -19,7 +19,7 @@ struct ChunkParams {
     // segments: tokens in each (0: whole sequences), their number, the states they
     // start from in accumulator order and their decay products, both [segment][head]
     int seg, segs;
-    int joined;  // a scan joins them; else every segment sums the ones before it (at most three)
+    int joined;  // a scan joins them; else every segment sums the ones before it
     float *ws, *wdec;
 };
 
@@ -39,7 +39,7 @@ inline ChunkParams chunk_params(const kda_linattn_prefill_args *a) {
 inline void use_segments(ChunkParams &p, const kda_linattn_prefill_args *a, const LinattnPlan &plan) {
     p.seg = plan.tokens;
     p.segs = (int)plan.segments;
-    p.joined = plan.longest > 4;
+    p.joined = plan.longest > kJoinSegments;
     p.ws = static_cast<float *>(a->workspace);
     p.wdec = p.ws + (size_t)(plan.segments + 1) * p.H * a->head_dim_k * p.dv;
 }

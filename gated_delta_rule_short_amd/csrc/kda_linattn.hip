@@ -22,7 +22,7 @@
 // values are read twice for it, first from the last chunk to the first: what the
 // outputs begin with was read last and is still cached (1 x 65,536 tokens x 8 heads
 // 202 -> 195 us, 1 x 4096 x 64 95 -> 91 us; and the state needs no decay on the way).
-// Segments of up to four to a sequence are joined by the third launch itself.
+// Where sequences have few segments, the third launch joins them itself.
 //
 // Rounding: P and the state under q are rounded to bf16 once as operands (the
 // outputs are bf16 themselves).  The decayed values of the state's own product
@@ -355,6 +355,7 @@ __global__ void __launch_bounds__((Lay<DK, DVT, DKS, NS, OUT>::THREADS), (NS == 
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 S[u][e] = *reinterpret_cast<const f32x4 *>(p.ws + wbase - first * wnext + (2 * u + e) * 256);
+#pragma unroll 2
         for (int b = first - 1; b >= 0; --b) {
             const float d = p.wdec[(size_t)(wk.s - b - 1) * p.H + wk.h];
 #pragma unroll

@@ -100,12 +100,16 @@ int64_t longest_sequence(const kda_linattn_prefill_args &a, int64_t unknown) {
 }
 
 // Segments of the two-pass schedule: whole chunks of 64 tokens, one workgroup for each
-// of the 256 compute units (bf16: whole states) or two (fp32: 32 columns).
+// of the 256 compute units (bf16: whole states; fp32: 64 columns), or two in fp32 where
+// a segment keeps 256 tokens (1 sequence of 8192 tokens x 16 heads 216 -> 199 us,
+// 1 x 1024 x 64 100 -> 91; shorter ones cost more than they fill: 1 x 32,768 x 1 77 -> 87).
 kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
-    const int64_t groups = a.dtype == KDA_BF16 ? 256 : 512 / std::max(a.head_dim_v / 32, 1);
+    const int64_t work = (T + 63) / 64 * H;  // chunks of all heads
+    int64_t groups = a.dtype == KDA_BF16 ? 256 : 512 / std::max(a.head_dim_v / 64, 1);
+    if (a.dtype != KDA_BF16 && work < 4 * groups) groups /= 2;
     kda::LinattnPlan plan;
-    const int64_t chunks = ((T + 63) / 64 * H + groups - 1) / groups;  // in each
+    const int64_t chunks = (work + groups - 1) / groups;  // in each
     plan.tokens = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), (int64_t)1 << 24) * 64;
     plan.segments = T / plan.tokens + N;
     plan.bytes = ((size_t)(plan.segments + 1) * a.head_dim_k * a.head_dim_v + (size_t)plan.segments) * H * 4;
@@ -118,17 +122,20 @@ kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
 // follow one another; segments run side by side but read the keys and values twice, in
 // two more launches:
 //   bf16  one pass  5 + 1.33 longest / 64 (32-column tiles; 2.4 for whole states)
-//         two       14 + 0.045 pairs + 3.9 L / 64
-//   fp32  one pass  4 + 6.2 longest / 64;  two  18 + 11.7 L / 64
+//         two       10.5 + 0.045 pairs + 3.9 L / 64, and 3.5 for a launch that joins
+//   fp32  one pass  4 + 6.2 longest / 64 (8.1 with 64 columns)
+//         two        7 + 12 L / 64 (20 with two workgroups to a compute unit)
 // 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads 27/27, 47/34, 88/41,
-// 680/106; 64 heads 30/42, 52/58, 96/87, -; fp32, 8 heads 103/34, 204/47, 405/74, 3190/453.
+// 680/106; 64 heads 30/42, 52/58, 96/87, -; fp32, 8 heads 107/33, 211/44, 414/68, 3289/404.
 bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
     if (plan.bytes > KDA_PREFILL_WORKSPACE_CAP) return false;
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads, L = plan.tokens;
     const int64_t longest = longest_sequence(a, (T + N - 1) / N);  // the average where lengths are not known
-    if (a.dtype == KDA_F32) return 10 * longest > 19 * L + 2000;
-    const bool wide = N * H * (a.head_dim_v / 64) >= 256;
-    return (wide ? 240 : 133) * longest > 390 * L + 290 * (T / L * H) + 57600;
+    const int64_t halves = N * H * (a.head_dim_v / 64);
+    if (a.dtype == KDA_F32)
+        return (halves > 128 ? 81 : 62) * longest > (L < 256 || T / L * H * (a.head_dim_v / 64) <= 256 ? 120 : 200) * L + 2000;
+    const bool wide = halves >= 256;
+    return (wide ? 240 : 133) * longest > 390 * L + 290 * (T / L * H) + (plan.longest > kda::kJoinSegments ? 57600 : 35200);
 }
 
 // Whether a call with a workspace runs two passes, and how (tokens 0: one pass).

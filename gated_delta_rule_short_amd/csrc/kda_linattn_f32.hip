@@ -4,11 +4,15 @@
 // The sums are those of kda_linattn.hip over chunks of 32 tokens, on the fp32 matrix
 // instructions (no operand is rounded; at 157 TFLOP/s the chip's fp32 rate is a
 // sixteenth of its bf16 rate, so a shorter chunk with fewer products inside it pays).
-// A workgroup of four waves carries 32 columns of a (sequence, head) state: wave w
-// makes the outputs of token block w / 2 and column tile w % 2, and holds the state
-// rows of every second 16-row tile of that column tile.  The state reaches the other
-// waves, and P the outputs, through LDS in operand order; q, k, v and g of the next
-// chunk are loaded into registers while the current one is worked on.
+// Those instructions are the bound of large calls: 16 sequences of 4096 tokens x 64 heads
+// x 128 x 128, 354 GFLOP with P formed for each half of the columns, take 3.4 ms, 104
+// TFLOP/s of the 143 that a large fp32 product reaches; with few heads the bound is a
+// chunk's chain of three barriers, 3.2 us, which segments shorten.
+// A workgroup carries 32 or 64 columns of a (sequence, head) state, two waves to a tile
+// of 16: each makes the outputs of one block of 16 tokens, and holds the state rows of
+// every second 16-row tile.  The state reaches the other waves, and P the outputs,
+// through LDS in operand order; q, k, v and g of the next chunk are loaded into
+// registers while the current one is worked on.
 #include <type_traits>
 
 #include "kda_linattn.h"
@@ -17,7 +21,7 @@ namespace kda {
 
 namespace {
 
-constexpr int C = 32, DVT = 32, VP = DVT + 4;
+constexpr int C = 32;
 
 __device__ __forceinline__ bool finite4(f32x4 x) {
     const f32x4 z = x * 0.f;  // NaN where x is not finite
@@ -30,19 +34,21 @@ template <bool BAD> __device__ __forceinline__ float part_of(float x) {
 }
 
 // OUT false: a segment's state alone, without q, P and outputs.
-template <int DK, bool OUT>
-__global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
+template <int DK, int DVT, bool OUT>
+__global__ void __launch_bounds__(8 * DVT) chunk_f32_kernel(ChunkParams p) {
+    constexpr int NCT = DVT / 16, NW = 2 * NCT;  // column tiles, waves
+    constexpr int VP = DVT + 4;
     constexpr int QP = DK + 4;          // row pitch: rows 4 apart fall on different banks
-    constexpr int QN = DK / 32;         // 16-byte pieces of a 32 x DK tensor per thread
+    constexpr int QN = DK / DVT;        // 16-byte pieces of a 32 x DK tensor per thread
     constexpr int NT = DK / 16, NH = NT / 2;  // 16-row tiles of the state, and per wave
     __shared__ __attribute__((aligned(16))) float lq[C * QP], lk[C * QP], lv[C * VP];
     __shared__ f32x4 lp[3][64];         // P blocks (0,0), (1,0), (1,1)
-    __shared__ f32x4 ls[2][NT][64];     // the state, operand order
+    __shared__ f32x4 ls[NCT][NT][64];     // the state, operand order
     __shared__ Factors fac;
-    __shared__ int bad[4];
+    __shared__ int bad[NW];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, g4 = lane >> 4, rt = wave >> 1, ct = wave & 1;
+    const int r16 = lane & 15, g4 = lane >> 4, rt = wave / NCT, ct = wave % NCT;
     Work wk;
     if (!locate(p, wk, lane)) return;
     if (!OUT && wk.j + 1 >= wk.nseg) return;  // nothing starts from the last segment
@@ -66,12 +72,13 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
             for (int i = 0; i < 4; ++i) S[j][i] = to_f32(x[sbase + (size_t)(32 * j + i) * p.dv]);
     };
     // where a segment starts from: see the workspace of kda_linattn.hip
-    float *ws = p.ws + ((size_t)wk.s * p.H + h) * DK * p.dv + (size_t)(tile * 4 + wave) * NH * 256 + lane * 4;
+    float *ws = p.ws + ((size_t)wk.s * p.H + h) * DK * p.dv + (size_t)(tile * NW + wave) * NH * 256 + lane * 4;
     const size_t next = (size_t)p.H * DK * p.dv;
     if (OUT && wk.nseg > 1) {
         const int first = p.joined || wk.j < 2 ? 0 : wk.j - 1;
 #pragma unroll
         for (int j = 0; j < NH; ++j) S[j] = *reinterpret_cast<const f32x4 *>(ws - first * next + j * 256);
+#pragma unroll 2
         for (int b = first - 1; b >= 0; --b) {
             const float x = p.wdec[(size_t)(wk.s - b - 1) * p.H + h];
 #pragma unroll
@@ -97,12 +104,12 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     // this thread's pieces of the next chunk (zeros past the sequence)
     f32x4 nq[QN], nk[QN], nv;
     float ng = 0.f;
-    const int vr = tid / 8, vc = 4 * (tid % 8);
+    const int vr = tid / (DVT / 4), vc = 4 * (tid % (DVT / 4));
     auto load = [&](int c) __attribute__((always_inline)) {
         const f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int e = tid + 256 * i, r = c * C + e / (DK / 4), d = 4 * (e % (DK / 4));
+            const int e = tid + 64 * NW * i, r = c * C + e / (DK / 4), d = 4 * (e % (DK / 4));
             if (OUT) nq[i] = r < len ? *reinterpret_cast<const f32x4 *>(q + r * p.qs + d) : z;
             nk[i] = r < len ? *reinterpret_cast<const f32x4 *>(k + r * p.ks + d) : z;
         }
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         const int m = min(len - c * C, C);
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int e = tid + 256 * i, at = e / (DK / 4) * QP + 4 * (e % (DK / 4));
+            const int e = tid + 64 * NW * i, at = e / (DK / 4) * QP + 4 * (e % (DK / 4));
             if (OUT) *reinterpret_cast<f32x4 *>(lq + at) = nq[i];
             *reinterpret_cast<f32x4 *>(lk + at) = nk[i];
         }
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         f32x4 d = {0.f, 0.f, 0.f, 0.f}, acc = d;
         if (wave == 3) {
             chunk_factors(gc, &fac, m, lane);
-        } else if (OUT) {
+        } else if (OUT && wave < 3) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const f32x4 a = *reinterpret_cast<const f32x4 *>(lk + (16 * ps + r16) * QP + 16 * t + 4 * g4);
@@ -173,7 +180,9 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
         const f32x4 p1 = lp[rt][lane], p2 = lp[2][lane];  // (rt, 0), (1, 1)
         // a value that is not finite is left out of the products, where zeros of the
         // future would not stay zeros, and added to the rows that see it
-        const bool odd = bad[0] | bad[1] | bad[2] | bad[3];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) odd |= bad[i];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = mma_f32(odd ? part_of<false>(vt[0][i]) : vt[0][i], p1[i], acc);
         if (rt == 1) {
@@ -235,28 +244,39 @@ __global__ void __launch_bounds__(256) chunk_f32_kernel(ChunkParams p) {
     else write(static_cast<float *>(p.s_out));
 }
 
-template <bool OUT> hipError_t launch(const ChunkParams &p, int dk, hipStream_t s) {
+template <int DVT, bool OUT> hipError_t launch(ChunkParams p, int dk, hipStream_t s) {
+    p.tiles = p.dv / DVT;
     const unsigned blocks = (unsigned)((p.units + 7) / 8) * 8 * p.rep * p.tiles;
-    if (dk == 64) hipLaunchKernelGGL((chunk_f32_kernel<64, OUT>), dim3(blocks), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((chunk_f32_kernel<128, OUT>), dim3(blocks), dim3(256), 0, s, p);
-    trace("chunk_f32_kernel<%d, %d> grid=(%u) block=256", dk, (int)OUT, blocks);
+    if (dk == 64) hipLaunchKernelGGL((chunk_f32_kernel<64, DVT, OUT>), dim3(blocks), dim3(8 * DVT), 0, s, p);
+    else hipLaunchKernelGGL((chunk_f32_kernel<128, DVT, OUT>), dim3(blocks), dim3(8 * DVT), 0, s, p);
+    trace("chunk_f32_kernel<%d, %d, %d> grid=(%u) block=%d", dk, DVT, (int)OUT, blocks, 8 * DVT);
     return hipGetLastError();
+}
+template <int DVT> hipError_t launch(ChunkParams &p, const kda_linattn_prefill_args *a, const LinattnPlan &plan,
+                                     hipStream_t s) {
+    if (plan.tokens) {
+        use_segments(p, a, plan);
+        hipError_t e = launch<DVT, false>(p, a->head_dim_k, s);
+        if (e != hipSuccess) return e;
+        e = p.joined ? launch_segment_scan(p, a->head_dim_k * p.dv, s) : hipSuccess;
+        if (e != hipSuccess) return e;
+    }
+    return launch<DVT, true>(p, a->head_dim_k, s);
 }
 
 }  // namespace
 
 hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPlan &plan, hipStream_t s) {
     ChunkParams p = chunk_params(a);
-    p.tiles = p.dv / DVT;
     p.units = (plan.tokens ? (int)plan.segments : p.N) * a->num_k_heads;
-    if (plan.tokens) {
-        use_segments(p, a, plan);
-        hipError_t e = launch<false>(p, a->head_dim_k, s);
-        if (e != hipSuccess) return e;
-        e = p.joined ? launch_segment_scan(p, a->head_dim_k * p.dv, s) : hipSuccess;
-        if (e != hipSuccess) return e;
-    }
-    return launch<true>(p, a->head_dim_k, s);
+    // 32 columns while a compute unit has one workgroup at most; beyond it 64, which form
+    // P half as often.  dk = dv = 128, one pass, us (32/64 columns): 16 heads of 2048
+    // tokens 208/254, 128 heads of 256 tokens 43/38, 1024 heads of 1024 4542/3392.  The
+    // segment numbers that several sequences leave unused crowd the others on fewer units:
+    // two passes, dk 64, 256 workgroups of 64 columns: one sequence 162/149, four 336/387.
+    const int64_t states = (plan.tokens ? p.total / plan.tokens : p.N) * (int64_t)p.H;
+    const int64_t narrow = plan.tokens && p.N > 1 ? 256 : 128;
+    return states * (p.dv / 64) > narrow ? launch<64>(p, a, plan, s) : launch<32>(p, a, plan, s);
 }
 
 }  // namespace kda

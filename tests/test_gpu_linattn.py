@@ -78,6 +78,21 @@ def test_prefill_two_passes(dk, dv, lengths, pool, dtype):
     assert torch.equal(o, o1) and torch.equal(st[rows], st1[rows])
 
 
+@pytest.mark.parametrize("lengths,host,dk,dv", [([1500], True, 128, 128), ([3800, 3, 1300], False, 64, 128),
+                                                ([2100, 0, 70], True, 128, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_two_passes_of_many_segments(lengths, host, dk, dv, dtype):
+    """Segments joined by the launch that makes the outputs, or by one of their own, over
+    enough heads that a workgroup takes more columns; a cleared state among them."""
+    inp = make_linattn(lengths, 12, 4, dk, dv, dtype, seed=90 + len(lengths), device=DEV)
+    inp["log_decay"][len(inp["q"]) // 2, 5] = float("-inf")
+    ref = dict(inp, state=inp["state"].clone())
+    o, st = kda.kda_linattn_prefill(inp["q"], inp["k"], inp["v"], inp["log_decay"], cu_seqlens=inp["cu"],
+                                    cu_seqlens_host=inp["cu_host"] if host else None, state_in=inp["state"],
+                                    state_out=inp["state"], schedule="two_pass")
+    check_linattn(o, st, ref, True)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_prefill_automatic_segments(dtype):
     """A long lone sequence takes two passes by itself; the outputs agree with one pass
