@@ -100,14 +100,16 @@ int64_t longest_sequence(const kda_linattn_prefill_args &a, int64_t unknown) {
 }
 
 // Segments of the two-pass schedule: whole chunks of 64 tokens, one workgroup for each
-// of the 256 compute units (bf16: whole states; fp32: 64 columns), or two in fp32 where
-// a segment keeps 256 tokens (1 sequence of 8192 tokens x 16 heads 216 -> 199 us,
-// 1 x 1024 x 64 100 -> 91; shorter ones cost more than they fill: 1 x 32,768 x 1 77 -> 87).
+// of the 256 compute units (bf16: whole states; fp32: 64 columns).  Two fit one unit,
+// except of 128-column states in bf16, and are taken where a segment keeps 256 tokens
+// (fp32, 1 sequence of 8192 tokens x 16 heads 216 -> 199 us, bf16 x 64 columns, 2
+// sequences of 13,438 tokens x 15 heads 67 -> 59; shorter ones cost more than they fill:
+// fp32 1 x 32,768 x 1 77 -> 87, bf16 36 of 31,407 x 2 34 -> 44).
 kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
     const int64_t work = (T + 63) / 64 * H;  // chunks of all heads
-    int64_t groups = a.dtype == KDA_BF16 ? 256 : 512 / std::max(a.head_dim_v / 64, 1);
-    if (a.dtype != KDA_BF16 && work < 4 * groups) groups /= 2;
+    int64_t groups = a.dtype == KDA_F32 && a.head_dim_v > 64 ? 256 : 512;
+    if ((a.dtype == KDA_BF16 && a.head_dim_v > 64) || work < 4 * groups) groups /= 2;
     kda::LinattnPlan plan;
     const int64_t chunks = (work + groups - 1) / groups;  // in each
     plan.tokens = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), (int64_t)1 << 24) * 64;

@@ -174,6 +174,9 @@ struct GatedParams {
     float eps;
 };
 
+// One row of one head.  16,384 tokens x 64 heads x 128 in bf16 with the gate (805 MB
+// moved): 142 us, 5.65 TB/s, above the 5.2 of a large copy, which writes half of what it
+// moves where this writes a third.
 template <typename T, int D>
 __device__ __forceinline__ void gated_row(const GatedParams &p, int64_t r, int c0) {
     const int64_t t = r / p.H;
