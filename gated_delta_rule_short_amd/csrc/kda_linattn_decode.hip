@@ -1,18 +1,17 @@
 // kda_linattn_decode.hip -- one token of the linear attention with one decay per
 // head: S <- exp(min(g, 0)) S + k v^T, o = scale S^T q.
 //
-// A workgroup of 256 threads owns 64 columns of one (sequence, head) state: the
-// columns of a state never mix, so any split over them is exact.  The state stays in
-// registers from its read to its write; thread t owns 16 bytes of neighbouring
+// A workgroup of four threads to a column owns 64 or 128 columns of one (sequence, head)
+// state: the columns of a state never mix, so any split over them is exact.  The state
+// stays in registers from its read to its write; thread t owns 16 bytes of neighbouring
 // columns in rows t / LPR + RG m.  Per element: one multiply and two FMAs (the decay,
 // the write k v, the read q); the column sums cross the lanes of a wave, then the
 // waves through LDS.
 //
 // The bound is HBM: every state is read once and written once, with non-temporal
 // accesses (a step's states are not read again before every other layer's).  256
-// sequences x 64 heads of fp32 states (2.16 GB): 373 us, 5.8 TB/s, against 5.9 TB/s of
-// a bare read-and-write-back of such states; 409 us without the hint, and 398 us (128
-// columns, 512 threads) or 389 us (32 columns) with it in other splits.
+// sequences x 64 heads of fp32 states (2.16 GB): 366 us, 5.9 TB/s, the rate of a bare
+// read-and-write-back of such states; 409 us without the hint.
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -56,14 +55,14 @@ template <> struct StateVec<__bf16> {
     }
 };
 
-template <typename T, typename S, int DK>
-__global__ void __launch_bounds__(256) decode_kernel(DecodeParams p) {
-    constexpr int VEC = StateVec<S>::N, DVT = 64;
+template <typename T, typename S, int DK, int DVT>
+__global__ void __launch_bounds__(4 * DVT) decode_kernel(DecodeParams p) {
+    constexpr int VEC = StateVec<S>::N, WAVES = DVT / 16;
     constexpr int LPR = DVT / VEC;     // lanes of a state row
-    constexpr int RG = 256 / LPR;      // rows held side by side
+    constexpr int RG = 4 * DVT / LPR;     // rows held side by side
     constexpr int M = DK / RG;         // rows per thread
     static_assert(M * RG == DK, "thread layout");
-    __shared__ float sq[DK], sk[DK], part[4][DVT];
+    __shared__ float sq[DK], sk[DK], part[WAVES][DVT];
     const int tid = threadIdx.x, tile = blockIdx.x % p.tiles;
     const int pair = blockIdx.x / p.tiles, n = pair / p.H, h = pair - n * p.H;
     const int slot = pool_slot(p.slots, p.num_slots, n);
@@ -108,16 +107,24 @@ __global__ void __launch_bounds__(256) decode_kernel(DecodeParams p) {
         for (int i = 0; i < VEC; ++i) part[tid / 64][cl * VEC + i] = acc[i];
     }
     __syncthreads();
-    if (tid < DVT)
-        static_cast<T *>(p.o)[((size_t)n * p.H + h) * p.dv + tile * DVT + tid] =
-            from_f32<T>((part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]));
+    if (tid < DVT) {
+        float o = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        if constexpr (WAVES == 8) o += (part[4][tid] + part[5][tid]) + (part[6][tid] + part[7][tid]);
+        static_cast<T *>(p.o)[((size_t)n * p.H + h) * p.dv + tile * DVT + tid] = from_f32<T>(o);
+    }
 }
 
-template <typename T, typename S, int DK> hipError_t launch(const DecodeParams &p, int N, hipStream_t s) {
+template <typename T, typename S, int DK, int DVT> hipError_t launch(DecodeParams p, int N, hipStream_t s) {
+    p.tiles = p.dv / DVT;
     const unsigned blocks = (unsigned)N * p.H * p.tiles;
-    hipLaunchKernelGGL((decode_kernel<T, S, DK>), dim3(blocks), dim3(256), 0, s, p);
-    trace("decode_kernel<dk=%d> grid=(%u) block=256", DK, blocks);
+    hipLaunchKernelGGL((decode_kernel<T, S, DK, DVT>), dim3(blocks), dim3(4 * DVT), 0, s, p);
+    trace("decode_kernel<dk=%d, %d columns> grid=(%u) block=%d", DK, DVT, blocks, 4 * DVT);
     return hipGetLastError();
+}
+// 128 columns where there are states enough, us (64/128 columns, 512 threads): 64 heads, 1
+// sequence 3.2/3.6, 4 6.1/6.6, 8 12.9/12.4, 256 373/366, with bf16 states 187/175.
+template <typename T, typename S, int DK> hipError_t launch(const DecodeParams &p, int N, hipStream_t s) {
+    return p.dv == 128 && (int64_t)N * p.H >= 512 ? launch<T, S, DK, 128>(p, N, s) : launch<T, S, DK, 64>(p, N, s);
 }
 template <typename T> hipError_t launch(const DecodeParams &p, const kda_linattn_decode_args *a, hipStream_t s) {
     const int N = a->num_seqs;
@@ -136,7 +143,7 @@ hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s
     p.H = a->num_heads; p.rep = a->num_heads / a->num_k_heads;
     p.qs = a->q_stride; p.ks = a->k_stride; p.vs = a->v_stride;
     p.gs = (a->flags & KDA_F_DECAY_PER_HEAD) ? 0 : a->num_heads;
-    p.dv = a->head_dim_v; p.tiles = p.dv / 64; p.scale = a->scale;
+    p.dv = a->head_dim_v; p.scale = a->scale;
     return a->dtype == KDA_BF16 ? launch<__bf16>(p, a, s) : launch<float>(p, a, s);
 }
 

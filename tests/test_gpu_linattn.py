@@ -245,6 +245,19 @@ def test_decode(N, H, Hk, dk, dv, dtype, state_dtype):
     assert torch.equal(inp["state"][rest], ref["state"][rest])
 
 
+@pytest.mark.parametrize("dk,dtype,state_dtype", [(64, BF, F32), (128, BF, F32), (64, F32, BF), (128, BF, BF), (128, F32, F32)])
+def test_decode_many_states(dk, dtype, state_dtype):
+    """Enough (sequence, head) pairs for 128 columns to a workgroup, in a pool, out of order."""
+    inp = make_linattn([1] * 65, 8, 2, dk, 128, dtype, state_dtype, seed=110 + dk, pool=70, device=DEV)
+    ref = dict(inp, state=inp["state"].clone())
+    o = kda.kda_linattn_decode(inp["q"], inp["k"], inp["v"], inp["log_decay"], inp["state"],
+                               state_slots=inp["slots"])
+    rows = inp["slots"].long()
+    check_linattn(o, inp["state"][rows], ref, False)
+    rest = [i for i in range(70) if i not in rows.tolist()]
+    assert torch.equal(inp["state"][rest], ref["state"][rest])
+
+
 def test_decode_skips_slots_outside_the_pool():
     inp = make_linattn([1] * 4, 2, 2, 128, 128, seed=4, pool=6, device=DEV)
     before = inp["state"].clone()
