@@ -127,8 +127,8 @@ kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
 //         two       10.5 + 0.045 pairs + 3.9 L / 64, and 3.5 for a launch that joins
 //   fp32  one pass  4 + 6.2 longest / 64 (8.1 with 64 columns)
 //         two        7 + 12 L / 64 (20 with two workgroups to a compute unit)
-// 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads 27/27, 47/34, 88/41,
-// 680/106; 64 heads 30/42, 52/58, 96/87, -; fp32, 8 heads 107/33, 211/44, 414/68, 3289/404.
+// 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads 27/22, 47/33, 89/40,
+// 688/102; 64 heads 31/35, 53/50, 100/82, -; fp32, 8 heads 106/26, 209/39, 412/65, 3260/392.
 bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
     if (plan.bytes > KDA_PREFILL_WORKSPACE_CAP) return false;
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads, L = plan.tokens;
