@@ -187,7 +187,7 @@ kda_status linattn_prefill_impl(kda_linattn_prefill_args a, hipStream_t stream) 
     const size_t gb = (size_t)H * ((a.flags & KDA_F_DECAY_PER_HEAD) ? 1 : T) * 4;
     if (a.schedule != KDA_SCHEDULE_AUTO && a.schedule != KDA_SCHEDULE_ONE_PASS && a.schedule != KDA_SCHEDULE_TWO_PASS)
         return fail(KDA_ERR_UNSUPPORTED, "schedule %d: automatic, one pass or two passes", a.schedule);
-    if (a.schedule == KDA_SCHEDULE_TWO_PASS) {
+    if (a.schedule == KDA_SCHEDULE_TWO_PASS && T > 0) {  // (no tokens, no passes)
         if (!a.workspace)
             return fail(KDA_ERR_INVALID_ARG, "the two-pass schedule needs a workspace (kda_linattn_workspace_size)");
         if (N * H >= kMaxSegmentPairs) return fail(KDA_ERR_INVALID_ARG, "too many pairs for the two-pass schedule");
