@@ -751,9 +751,10 @@ def _rows(t, name, shape, dtype, dev):
 
 
 # The current stream of a device as an address (torch.cuda.current_stream makes an
-# object of it first, at 2 us), and the current device.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# object of it first, at 2 us), and the current device.  A torch build without GPU support
+# has neither, nor a tensor that gets as far as them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _elsewhere(dev, stream):

@@ -1,11 +1,15 @@
 """The linear-attention entry points at the edges of what the binding and the checks
-accept, without a GPU: calls with nothing to do."""
+accept, without a GPU: calls with nothing to do, and a torch build that knows no GPU."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
 
 from gated_delta_rule_short_amd import kda as K
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -24,3 +28,27 @@ def test_an_empty_batch_needs_no_workspace(lib, schedule):
                                 dtype=K.KDA_BF16, total_tokens=0, schedule=schedule)
     assert lib.kda_linattn_workspace_size(ctypes.byref(a)) == 0
     assert lib.kda_linattn_prefill(ctypes.byref(a), None) == K.KDA_OK
+
+
+def test_import_on_a_torch_without_gpu_support():
+    """A torch build without GPU support lacks its device and stream functions: the package
+    still imports, and host tensors are refused as elsewhere."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+import gated_delta_rule_short_amd as kda
+q = torch.zeros(2, 1, 64)
+for call in (lambda: kda.kda_gated_norm(q), lambda: kda.kda_qk_norm_rope(q, q),
+             lambda: kda.kda_linattn_prefill(q, q, q, torch.zeros(2, 1)),
+             lambda: kda.kda_linattn_decode(q, q, q, torch.zeros(2, 1), torch.zeros(2, 1, 64, 64))):
+    try:
+        call()
+    except ValueError as e:
+        assert "GPU" in str(e), e
+    else:
+        raise AssertionError("accepted")
+print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr[-2000:]
