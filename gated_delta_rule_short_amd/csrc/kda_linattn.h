@@ -106,9 +106,11 @@ __device__ __forceinline__ bool locate(const ChunkParams &p, Work &w, int lane) 
 
 constexpr int kFactorTokens = 64;  // most tokens of a chunk
 
-// Factors of one chunk: bh + bl (the decay sums, base 2), eb = 2^b, w = 2^(b_n - b)
-// (0 past the sequence), 2^(b_n) last; w and the last also over `after`, the sum of
-// the chunks behind it.
+// Factors of one chunk: bh + bl (the decay sums, base 2), eb = 2^b, w = 2^(b_n - b), 2^(b_n)
+// last; w and the last also over `after`, the sum of the chunks behind it.  Rows past the
+// sequence repeat its last token, whose w is 1, or hold zeros: their w of 2^-60 adds 2^-54 of
+// that token's product at most, which fp32 does not see, where a zero would make NaN of an
+// infinity in it.
 struct Factors {
     float bh[kFactorTokens], bl[kFactorTokens], eb[kFactorTokens], w[kFactorTokens], total, pad[3];
 };
@@ -147,7 +149,7 @@ __device__ __forceinline__ double chunk_factors(float x, Factors *f, int n, int 
     f->bh[lane] = hi;
     f->bl[lane] = (float)(b - (double)hi);
     f->eb[lane] = exp2_fast(hi);
-    f->w[lane] = lane < n ? exp2_fast((float)(e - b + after)) : 0.f;
+    f->w[lane] = lane < n ? exp2_fast((float)(e - b + after)) : 0x1p-60f;
     if (lane == 0) f->total = exp2_fast((float)(e + after));
     return e;
 }
