@@ -228,10 +228,6 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _dtype_code(t):
     if t.dtype == torch.bfloat16:
         return KDA_BF16
