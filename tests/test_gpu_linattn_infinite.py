@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_delta_rule_short_amd as kda
-from tests._linattn_common import DEV, U16, U32, TINY, check, half_step, linattn_ref, make_linattn
+from tests._linattn_common import DEV, U16, U32, TINY, check, check_linattn, half_step, linattn_ref, make_linattn
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -85,3 +85,24 @@ def test_decode_states_keep_infinities(dtype, state_dtype):
         assert torch.equal(torch.isinf(state.cpu()), torch.isinf(ref)) and torch.equal(torch.isnan(state.cpu()), torch.isnan(ref))
     else:
         _check_states(state, inp, "decode")
+
+
+@pytest.mark.parametrize("schedule", ["one_pass", "two_pass"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_products_that_underflow_stay_numbers(schedule, dtype):
+    """Tiny values of both signs under decays of every size, zeros of both signs, and a
+    whole sequence of such: their products round to zero and change nothing else."""
+    inp = make_linattn([200, 64, 1], 3, 3, 128, 128, dtype, seed=77, device=DEV)
+    g = torch.Generator().manual_seed(78)
+    power = torch.randint(-126, 0, (265, 3, 128), generator=g).to(DEV)
+    tiny = torch.exp2(power.float()) * torch.where(inp["v"].float() < 0, -1.0, 1.0)
+    pick = torch.rand(265, 3, 128, generator=g).to(DEV)
+    v = torch.where(pick < 0.4, tiny, torch.where(pick < 0.5, 0.0, torch.where(pick < 0.6, -0.0, inp["v"].float())))
+    v[200:264, 1] = tiny[200:264, 1]
+    inp["v"] = v.to(dtype)
+    inp["log_decay"][:, 0] = -2.0  # e^-128 over a chunk
+    inp["log_decay"][::9, 1] = -60.0
+    o, st = kda.kda_linattn_prefill(inp["q"], inp["k"], inp["v"], inp["log_decay"], cu_seqlens=inp["cu"],
+                                    cu_seqlens_host=inp["cu_host"], state_in=inp["state"], state_out=True,
+                                    schedule=schedule)
+    check_linattn(o, st, inp, True)
