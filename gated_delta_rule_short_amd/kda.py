@@ -803,8 +803,12 @@ def kda_linattn_prefill(q, k, v, log_decay, *, cu_seqlens=None, cu_seqlens_host=
     with state_slots (int32 [N]) the state tensors are pools and sequence n uses row
     state_slots[n].  state_out: a tensor, or True to allocate one of state_in's dtype
     (else fp32).  scale 0 is 1 / sqrt(dk).  schedule: "auto", "one_pass" or "two_pass"
-    (include/kda.h); workspace: True allocates what the schedule needs, a uint8 tensor is
-    used, None or False gives none (one pass).  Returns (o [T, H, dv], state_out)."""
+    (include/kda.h); "auto" knows the longest sequence only from cu_seqlens_host (or equal
+    sequences): without it, one long sequence among short ones is better asked "two_pass".
+    workspace: True allocates what the schedule needs, a uint8 tensor is used, None or False
+    gives none (one pass).  bf16 tokens round the scores and the state under q to bf16
+    once, fp32 tokens nothing below fp32; the states are fp32 sums either way.  Returns
+    (o [T, H, dv], state_out)."""
     lib = _lib or load_library()
     dev, dt = q.device, q.dtype
     T, Hk, dk, H, dv = _linattn_shapes(q, v)
