@@ -22,7 +22,7 @@
 // the outputs with every segment starting from its scanned state.  The keys and
 // values are read twice for it, first from the last chunk to the first: what the
 // outputs begin with was read last and is still cached (1 x 65,536 tokens x 8 heads
-// 202 -> 195 us, 1 x 4096 x 64 95 -> 91 us; and the state needs no decay on the way).
+// 202 -> 197 us, 1 x 4096 x 64 92.6 -> 92.2; and the state needs no decay on the way).
 // Where sequences have few segments, the third launch joins them itself.
 //
 // Rounding: P and the state under q are rounded to bf16 once as operands (the
@@ -32,10 +32,12 @@
 // decay sums run in 64 bits and are kept as two floats: b_r - b_s stays exact
 // behind a token that clears the state (a large |g|).
 //
-// What bounds it: 16 sequences of 4096 tokens x 64 heads x 128 x 128 (4.3 GB) take 1.02
-// to 1.27 ms, 3.4 to 4.2 TB/s against 5.2 of a large copy, at 1.2 to 1.6 GHz: the power
+// What bounds it: 16 sequences of 4096 tokens x 64 heads x 128 x 128 (4.3 GB) take 0.98
+// to 1.27 ms, 3.4 to 4.4 TB/s against 5.2 of a large copy, at 1.2 to 1.6 GHz: the power
 // that the state's products draw (0.91 ms at 2.3 GHz without them).  A lone sequence is
-// bound by the chain of its chunks, 1.33 us each.
+// bound by the chain of its chunks, 1.4 us each; cut into many segments, by the scan that
+// joins them, whose steps of eight segments follow one another at 1.25 us (1 x 16,384
+// tokens x 1 head: 256 segments, 53 us).
 //
 // A future token has a zero in P, but zero times a non-finite value is not
 // zero: products never run over whole 16-token blocks of the future, and a NaN or
@@ -620,7 +622,7 @@ hipError_t launch_wide(const ChunkParams &p, int dk, hipStream_t s) {
 }
 
 // Whole states over segments; of 64 columns two workgroups to a compute unit, with fewer
-// stages of loads in each (8 sequences of 36,559 tokens in all, 5 heads, dk 128 89 -> 60 us).
+// stages of loads in each (8 sequences of 36,559 tokens in all, 5 heads, dk 128 79 -> 73 us).
 template <bool OUT> hipError_t launch_segments(const ChunkParams &p, int dk, hipStream_t s) {
     constexpr int NS = OUT ? 3 : 4, NS64 = OUT ? 1 : 2;
     if (dk == 64) return p.dv == 128 ? launch<64, 128, 1, NS, OUT>(p, s) : launch<64, 64, 1, NS64, OUT>(p, s);
@@ -684,8 +686,9 @@ hipError_t launch_linattn_chunks(const kda_linattn_prefill_args *a, const Linatt
     const int64_t pairs = (int64_t)a->num_seqs * a->num_heads;
     // Many short sequences: one stage and 64 columns, so that a compute unit holds two
     // workgroups and one's loads run under the other's work.  640 workgroups (40
-    // sequences x 16 heads, dv 64) of 64 and 128 tokens each: dk 128 24.7 -> 15.6 and 31.6 ->
-    // 21.3 us, dk 64 17.7 -> 15.1 and 22.1 -> 20.0 us; no gain with 128 columns.
+    // sequences x 16 heads, dv 64, with states) of 64 and 128 tokens each, nothing cached: dk
+    // 128 26.7 -> 23.8 and 32.9 -> 33.7 us, dk 64 20.5 -> 15.3 and 25.6 -> 24.9; no gain with
+    // 128 columns.
     if (pairs >= 256 && p.dv == 64 && p.total <= 128 * (int64_t)p.N)
         return a->head_dim_k == 64 ? launch<64, 64, 1, 1, true>(p, s) : launch<128, 64, 1, 1, true>(p, s);
     if (pairs * (p.dv / 64) >= 256) return launch_wide(p, a->head_dim_k, s);

@@ -102,9 +102,9 @@ int64_t longest_sequence(const kda_linattn_prefill_args &a, int64_t unknown) {
 // Segments of the two-pass schedule: whole chunks of 64 tokens, one workgroup for each
 // of the 256 compute units (bf16: whole states; fp32: 64 columns).  Two fit one unit,
 // except of 128-column states in bf16, and are taken where a segment keeps 256 tokens
-// (fp32, 1 sequence of 8192 tokens x 16 heads 216 -> 199 us, bf16 x 64 columns, 2
-// sequences of 13,438 tokens x 15 heads 67 -> 59; shorter ones cost more than they fill:
-// fp32 1 x 32,768 x 1 77 -> 87, bf16 36 of 31,407 x 2 34 -> 44).
+// (fp32, 1 sequence of 8192 tokens x 16 heads 220 -> 195 us, bf16 x 64 columns, 2
+// sequences of 13,438 tokens x 15 heads 80 -> 76; shorter ones cost more than they fill:
+// fp32 1 x 32,768 x 1 77 -> 86, bf16 36 of 31,407 x 2 38 -> 44).
 kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads;
     const int64_t work = (T + 63) / 64 * H;  // chunks of all heads
@@ -119,7 +119,7 @@ kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
     return plan;
 }
 
-// The automatic choice, from the times of both sides (us; dk = dv = 128; L tokens and
+// The automatic choice compares a cost of both sides (us; dk = dv = 128; L tokens and
 // `pairs` segments x heads in two passes).  In one pass the longest sequence's chunks
 // follow one another; segments run side by side but read the keys and values twice, in
 // two more launches:
@@ -127,8 +127,13 @@ kda::LinattnPlan segment_plan(const kda_linattn_prefill_args &a) {
 //         two       10.5 + 0.045 pairs + 3.9 L / 64, and 3.5 for a launch that joins
 //   fp32  one pass  4 + 6.2 longest / 64 (8.1 with 64 columns)
 //         two        7 + 12 L / 64 (20 with two workgroups to a compute unit)
-// 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads 27/22, 47/33, 89/40,
-// 688/102; 64 heads 31/35, 53/50, 100/82, -; fp32, 8 heads 106/26, 209/39, 412/65, 3260/392.
+// The constants were fitted to calls on cached inputs.  Both sides on distinct tensors
+// that are not cached, 1 sequence of 1024, 2048, 4096 and 32,768 tokens, bf16: 8 heads
+// 28/22, 51/33, 99/40, 750/112; 64 heads 33/39, 59/58, 120/105, 939/632; fp32, 8 heads
+// 105/26, 209/40, 412/66, 3311/371.  There, over 1, 4 and 16 sequences x 1, 8, 16, 64 and 128
+// heads x 512 to 32,768 tokens, the choice is within 10 % of the better side but for bf16
+// 1 x 2048 x 128 (one pass 97, two 88), 16 x 1024 x 1 (28, 40), and 16 sequences x 8 heads from
+// 4096 tokens on (191, 244; of 16,384 705, 916), where it takes the other one.
 bool prefer_segments(const kda_linattn_prefill_args &a, const kda::LinattnPlan &plan) {
     if (plan.bytes > KDA_PREFILL_WORKSPACE_CAP) return false;
     const int64_t T = a.total_tokens, N = a.num_seqs, H = a.num_heads, L = plan.tokens;

@@ -10,7 +10,7 @@
 //
 // The bound is HBM: every state is read once and written once, with non-temporal
 // accesses (a step's states are not read again before every other layer's).  256
-// sequences x 64 heads of fp32 states (2.16 GB): 366 us, 5.9 TB/s, the rate of a bare
+// sequences x 64 heads of fp32 states (2.16 GB): 366 to 373 us, 5.9 TB/s, the rate of a bare
 // read-and-write-back of such states; 409 us without the hint.
 #include "kda_device.h"
 #include "kda_internal.h"
@@ -121,8 +121,9 @@ template <typename T, typename S, int DK, int DVT> hipError_t launch(DecodeParam
     trace("decode_kernel<dk=%d, %d columns> grid=(%u) block=%d", DK, DVT, blocks, 4 * DVT);
     return hipGetLastError();
 }
-// 128 columns where there are states enough, us (64/128 columns, 512 threads): 64 heads, 1
-// sequence 3.2/3.6, 4 6.1/6.6, 8 12.9/12.4, 256 373/366, with bf16 states 187/175.
+// 128 columns where there are states enough, us (64/128 columns, 512 threads; states not
+// cached): 64 heads, 1 sequence 4.3/5.0, 4 7.4/7.8, 8 13.5/13.2, 256 381/373, with bf16
+// states 195/182.
 template <typename T, typename S, int DK> hipError_t launch(const DecodeParams &p, int N, hipStream_t s) {
     return p.dv == 128 && (int64_t)N * p.H >= 512 ? launch<T, S, DK, 128>(p, N, s) : launch<T, S, DK, 64>(p, N, s);
 }

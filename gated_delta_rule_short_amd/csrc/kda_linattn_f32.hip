@@ -5,8 +5,8 @@
 // instructions (no operand is rounded; at 157 TFLOP/s the chip's fp32 rate is a
 // sixteenth of its bf16 rate, so a shorter chunk with fewer products inside it pays).
 // Those instructions are the bound of large calls: 16 sequences of 4096 tokens x 64 heads
-// x 128 x 128, 354 GFLOP with P formed for each half of the columns, take 3.4 ms, 104
-// TFLOP/s of the 143 that a large fp32 product reaches; with few heads the bound is a
+// x 128 x 128, 354 GFLOP with P formed for each half of the columns, take 3.4 to 3.5 ms, 104
+// to 101 TFLOP/s of the 143 that a large fp32 product reaches; with few heads the bound is a
 // chunk's chain of three barriers, 3.2 us, which segments shorten.
 // A workgroup carries 32 or 64 columns of a (sequence, head) state, two waves to a tile
 // of 16: each makes the outputs of one block of 16 tokens, and holds the state rows of
@@ -271,9 +271,10 @@ hipError_t launch_linattn_f32(const kda_linattn_prefill_args *a, const LinattnPl
     p.units = (plan.tokens ? (int)plan.segments : p.N) * a->num_k_heads;
     // 32 columns while a compute unit has one workgroup at most; beyond it 64, which form
     // P half as often.  dk = dv = 128, one pass, us (32/64 columns): 16 heads of 2048
-    // tokens 208/254, 128 heads of 256 tokens 43/38, 1024 heads of 1024 4542/3392.  The
+    // tokens 211/257, 128 heads of 256 tokens 47/41, 1024 heads of 4096 4638/3505.  The
     // segment numbers that several sequences leave unused crowd the others on fewer units:
-    // two passes, dk 64, 256 workgroups of 64 columns: one sequence 162/149, four 336/387.
+    // two passes, 4096 tokens x 8 heads, 256 workgroups of 64 columns: one sequence 66/61,
+    // four 66/88; dk 64 45/44 and 50/58.
     const int64_t states = (plan.tokens ? p.total / plan.tokens : p.N) * (int64_t)p.H;
     const int64_t narrow = plan.tokens && p.N > 1 ? 256 : 128;
     return states * (p.dv / 64) > narrow ? launch<64>(p, a, plan, s) : launch<32>(p, a, plan, s);
