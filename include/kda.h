@@ -507,8 +507,8 @@ size_t kda_gate_beta_workspace_size(const kda_gate_beta_args *args);
  * A non-finite q, k, v or g reaches the outputs of its own and later tokens of
  * its sequence and head, and no others.
  * An infinite k or v leaves infinities (or NaN, where the recurrence has them)
- * in the state; one may become NaN behind decays that multiply to less than
- * 2^-126.
+ * in the state; one may become NaN where the key or value that it meets, times
+ * the decays behind it, is below 2^-50.
  */
 #define KDA_F_DECAY_PER_HEAD 256u
 
