@@ -22,10 +22,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
-SOURCES = ["kda_api.hip", "kda_conv.hip", "kda_decode.hip", "kda_gate_proj.hip", "kda_linattn.hip",
+SOURCES = ["kda_add_norm.hip", "kda_api.hip", "kda_conv.hip", "kda_decode.hip", "kda_gate_proj.hip", "kda_linattn.hip",
            "kda_linattn_api.hip", "kda_linattn_decode.hip", "kda_linattn_f32.hip", "kda_norm.hip",
            "kda_pool.hip",
-           "kda_prefill.hip", "kda_prefill_split.hip"]
+           "kda_prefill.hip", "kda_prefill_split.hip", "kda_scan.hip", "kda_scan_api.hip", "kda_scan_decode.hip"]
 # measurement-only streaming kernels (include/kda_calib.h), a library of their own
 CALIB_LIB = os.path.join(PKG, "libkda_calib.so")
 CALIB_SOURCES = ["kda_calib.hip"]

@@ -86,4 +86,21 @@ hipError_t launch_linattn_decode(const kda_linattn_decode_args *a, hipStream_t s
 hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t s);
 hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t s);
 
+// Gated scan: `chained` with its tiles (numbered over all sequences) and workspace, or one
+// pass.  scan_tile: tokens of a tile.
+struct ScanPlan {
+    bool chained;
+    int64_t tiles;
+    void *workspace;
+};
+int scan_tile(kda_dtype dt, bool backward);
+hipError_t launch_gated_scan(const kda_gated_scan_args *a, const ScanPlan &plan, hipStream_t s);
+hipError_t launch_gated_scan_backward(const kda_gated_scan_backward_args *a, const ScanPlan &plan, hipStream_t s);
+hipError_t launch_gated_scan_decode(const kda_gated_scan_decode_args *a, hipStream_t s);
+
+// Norm in front of the in-projections, and its gradients.
+size_t add_norm_backward_workspace_bytes(int64_t T, int C);
+hipError_t launch_add_norm(const kda_add_norm_args *a, hipStream_t s);
+hipError_t launch_add_norm_backward(const kda_add_norm_backward_args *a, hipStream_t s);
+
 }  // namespace kda

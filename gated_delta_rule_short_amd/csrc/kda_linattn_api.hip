@@ -14,55 +14,6 @@ namespace {
 
 using namespace kda::checks;
 
-// A [tokens][width] tensor with `stride` elements from one token to the next.
-struct Rows {
-    const void *p;
-    int64_t tokens, stride, width;
-    size_t elem;
-    const char *name;
-};
-
-size_t rows_bytes(const Rows &r) {
-    return r.p && r.tokens > 0 ? ((size_t)(r.tokens - 1) * (size_t)r.stride + (size_t)r.width) * r.elem : 0;
-}
-
-// Tensors of one stride that interleave without sharing an element (views of one
-// packed projection) do not overlap; any other pair is judged by its byte range.
-bool rows_overlap(const Rows &a, const Rows &b) {
-    if (!overlap(a.p, rows_bytes(a), b.p, rows_bytes(b))) return false;
-    const int64_t sa = a.stride * (int64_t)a.elem, sb = b.stride * (int64_t)b.elem;
-    if (sa != sb) return true;
-    int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % sa;
-    if (d < 0) d += sa;
-    return !(d >= a.width * (int64_t)a.elem && sa - d >= b.width * (int64_t)b.elem);
-}
-
-// Resolves a dense stride and checks what the kernels' 16-byte accesses need.
-kda_status check_rows(Rows &r) {
-    if (r.stride == 0) r.stride = r.width;
-    if (r.stride < r.width)
-        return fail(KDA_ERR_INVALID_ARG, "%s_stride = %lld, a token has %lld elements", r.name, (long long)r.stride,
-                    (long long)r.width);
-    if (r.stride > ((int64_t)1 << 40) / std::max<int64_t>(r.tokens, 1))
-        return fail(KDA_ERR_INVALID_ARG, "%s_stride = %lld is too large", r.name, (long long)r.stride);
-    if ((uintptr_t)r.p % 16 || (size_t)r.stride * r.elem % 16)
-        return fail(KDA_ERR_INVALID_ARG, "%s and its token stride must be 16-byte aligned", r.name);
-    return KDA_OK;
-}
-
-// The written tensors (the first n_written) against every other; `same` gives the
-// input a written tensor may be (equal pointer and stride), or -1.
-kda_status check_rows_written(const Rows *r, int n, int n_written, const int *same) {
-    for (int i = 0; i < n_written; ++i)
-        for (int j = 0; j < n; ++j) {
-            if (j == i || (j < n_written && j < i)) continue;
-            if (j >= n_written && same[i] == j && r[i].p == r[j].p && r[i].stride == r[j].stride) continue;
-            if (rows_overlap(r[i], r[j]))
-                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", r[i].name, r[j].name);
-        }
-    return KDA_OK;
-}
-
 // (Sequence, head) pairs of a grid, which holds a multiple of eight key heads.
 int64_t grid_pairs(int64_t N, int32_t H, int32_t Hk) { return (N * Hk + 7) / 8 * 8 * (H / Hk); }
 

@@ -21,6 +21,10 @@ KDA_F32, KDA_BF16 = 0, 1
 KDA_F_SILU, KDA_F_NO_QK_L2NORM, KDA_F_GATE_IS_LOG, KDA_F_STATE_BF16 = 1, 2, 4, 8
 KDA_F_DECAY_PER_HEAD, KDA_F_ROPE_INTERLEAVED, KDA_F_WEIGHT_PER_HEAD = 256, 512, 1024
 NORMS = {"none": 0, "rms": 1, "l2": 2}  # kda_norm
+GATE_KINDS = {"log": 0, "sigmoid": 1}  # kda_gate_kind
+INPUT_KINDS = {"plain": 0, "complement": 1, "norm": 2}  # kda_input_kind
+QUANTS = {"none": 0, "token": 1, "group": 2}  # kda_quant
+SCAN_SCHEDULES = {"auto": 0, "one_pass": 1, "chained": 4}  # kda_schedule, the gated scan's
 PREFILL_WORKSPACE_CAP = 4 << 30  # KDA_PREFILL_WORKSPACE_CAP
 PREFILL_SCRATCH_BYTES = 256 << 20  # KDA_PREFILL_SCRATCH_BYTES (kda_prefill_noalloc)
 
@@ -30,7 +34,10 @@ EXPORTS = ("kda_abi_version", "kda_set_spin_limit", "kda_status_string", "kda_la
            "kda_prefill_workspace_min_size", "kda_prefill_noalloc", "kda_decode", "kda_decode_multi",
            "kda_decode_commit", "kda_state_copy", "kda_gate_beta_proj",
            "kda_gate_beta_workspace_size", "kda_linattn_prefill", "kda_linattn_decode",
-           "kda_linattn_workspace_size", "kda_qk_norm_rope", "kda_gated_norm")
+           "kda_linattn_workspace_size", "kda_qk_norm_rope", "kda_gated_norm",
+           "kda_gated_scan_prefill", "kda_gated_scan_workspace_size", "kda_gated_scan_decode",
+           "kda_gated_scan_backward", "kda_gated_scan_backward_workspace_size", "kda_add_norm",
+           "kda_add_norm_backward", "kda_add_norm_backward_workspace_size")
 MAX_SPEC_TOKENS = 8
 UPDATE_FLOATS = 6 * 128  # floats per (sequence, head, token) update record
 
@@ -160,6 +167,56 @@ class KdaGatedNormArgs(ctypes.Structure):
     ]
 
 
+class KdaGatedScanArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", _c_i32), ("channels", _c_i32), ("total_tokens", _c_i64), ("dtype", ctypes.c_int),
+        ("gate_kind", ctypes.c_int), ("input_kind", ctypes.c_int), ("flags", _c_u32),
+        ("x_stride", _c_i64), ("gate_stride", _c_i64), ("o_stride", _c_i64),
+        ("x", _p), ("gate", _p), ("state_in", _p), ("state_out", _p), ("o", _p), ("cu_seqlens", _p),
+        ("cu_seqlens_host", _p), ("state_slots", _p), ("num_slots", _c_i32), ("schedule", _c_i32),
+        ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class KdaGatedScanDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", _c_i32), ("channels", _c_i32), ("dtype", ctypes.c_int), ("gate_kind", ctypes.c_int),
+        ("input_kind", ctypes.c_int), ("flags", _c_u32),
+        ("x_stride", _c_i64), ("gate_stride", _c_i64), ("o_stride", _c_i64),
+        ("x", _p), ("gate", _p), ("state", _p), ("o", _p), ("state_slots", _p), ("num_slots", _c_i32),
+    ]
+
+
+class KdaGatedScanBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", _c_i32), ("channels", _c_i32), ("total_tokens", _c_i64), ("dtype", ctypes.c_int),
+        ("gate_kind", ctypes.c_int), ("input_kind", ctypes.c_int), ("flags", _c_u32),
+        ("d_o_stride", _c_i64), ("gate_stride", _c_i64), ("o_stride", _c_i64), ("x_stride", _c_i64),
+        ("dx_stride", _c_i64), ("dgate_stride", _c_i64),
+        ("d_o", _p), ("gate", _p), ("o", _p), ("x", _p), ("state_in", _p), ("dstate_out", _p),
+        ("dx", _p), ("dgate", _p), ("dstate_in", _p), ("cu_seqlens", _p), ("cu_seqlens_host", _p),
+        ("schedule", _c_i32), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class KdaAddNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _c_i64), ("channels", _c_i32), ("dtype", ctypes.c_int), ("quant", ctypes.c_int),
+        ("eps", _c_f32), ("x_stride", _c_i64), ("residual_stride", _c_i64), ("residual_out_stride", _c_i64),
+        ("y_stride", _c_i64), ("x", _p), ("residual", _p), ("weight", _p), ("residual_out", _p), ("y", _p),
+        ("scale", _p),
+    ]
+
+
+class KdaAddNormBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _c_i64), ("channels", _c_i32), ("dtype", ctypes.c_int), ("eps", _c_f32),
+        ("dy_stride", _c_i64), ("s_stride", _c_i64), ("dresidual_stride", _c_i64), ("dx_stride", _c_i64),
+        ("dy", _p), ("s", _p), ("dresidual", _p), ("weight", _p), ("dx", _p), ("dweight", _p),
+        ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__("%s: %s" % (status, msg))
@@ -209,11 +266,15 @@ def load_library(path: str = LIB_PATH):
         lib.kda_state_copy.restype = ctypes.c_int
         lib.kda_state_copy.argtypes = [ctypes.POINTER(KdaStateCopyArgs), _p]
         # arguments packed into bytes (see _PREFILL_PACK) or a structure by reference
-        for f in ("kda_linattn_prefill", "kda_linattn_decode", "kda_qk_norm_rope", "kda_gated_norm"):
+        for f in ("kda_linattn_prefill", "kda_linattn_decode", "kda_qk_norm_rope", "kda_gated_norm",
+                  "kda_gated_scan_prefill", "kda_gated_scan_decode", "kda_gated_scan_backward", "kda_add_norm",
+                  "kda_add_norm_backward"):
             getattr(lib, f).restype = ctypes.c_int
             getattr(lib, f).argtypes = [_p, _p]
-        lib.kda_linattn_workspace_size.restype = ctypes.c_size_t
-        lib.kda_linattn_workspace_size.argtypes = [_p]
+        for f in ("kda_linattn_workspace_size", "kda_gated_scan_workspace_size",
+                  "kda_gated_scan_backward_workspace_size", "kda_add_norm_backward_workspace_size"):
+            getattr(lib, f).restype = ctypes.c_size_t
+            getattr(lib, f).argtypes = [_p]
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -1040,6 +1101,381 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, y=None
     if st:
         _check(lib, st)
     return y
+
+
+# ------------------------------------------------------------------ gated scan, norm with the residual
+_SCAN_PACK = struct.Struct("@2iq3iI3q8PiiPN")
+_STEP_PACK = struct.Struct("@5iI3q5Pi4x")
+_SCAN_GRAD_PACK = struct.Struct("@2iq3iI6q11PiPN")
+_ADD_NORM_PACK = struct.Struct("@q3if4q6P")
+_ADD_NORM_GRAD_PACK = struct.Struct("@qiif4q7PN")
+
+
+def _rows2(t, name, shape, dtype, dev):
+    """Token stride of a [T, C] tensor whose channels are dense (0: dense tokens too)."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+    if t.is_contiguous():
+        return 0
+    T, C = shape
+    st, sd = t.stride()
+    if sd != 1:
+        raise ValueError("the channels of %s must be dense: strides %s" % (name, t.stride()))
+    if T == 1:
+        return 0
+    if st < C:
+        raise ValueError("the tokens of %s must not overlap: strides %s" % (name, t.stride()))
+    return st
+
+
+def _kinds(gate_kind, input_kind):
+    gk, ik = GATE_KINDS.get(gate_kind), INPUT_KINDS.get(input_kind)
+    if gk is None:
+        raise ValueError("gate_kind must be one of %s" % sorted(GATE_KINDS))
+    if ik is None:
+        raise ValueError("input_kind must be one of %s" % sorted(INPUT_KINDS))
+    return gk, ik
+
+
+def _scan_schedule(schedule):
+    code = SCAN_SCHEDULES.get(schedule) if isinstance(schedule, str) else int(schedule)
+    if code is None:
+        raise ValueError("schedule must be one of %s" % sorted(SCAN_SCHEDULES))
+    return code
+
+
+def _cu(cu_seqlens, cu_seqlens_host, num_seqs, dev):
+    """(N, device address, host tensor or None) of the sequences' bounds."""
+    N, cup = int(num_seqs or 1), 0
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        N = cu_seqlens.numel() - 1
+        _shape(cu_seqlens, "cu_seqlens", (N + 1,))
+        cup = cu_seqlens.data_ptr()
+    cuh = cu_seqlens_host
+    if cuh is not None:
+        if not (torch.is_tensor(cuh) and cuh.dtype is torch.int32 and cuh.is_cpu and cuh.is_contiguous()):
+            cuh = torch.as_tensor(cuh, dtype=torch.int32, device="cpu").contiguous()
+        _shape(cuh, "cu_seqlens_host", (N + 1,))
+    return N, cup, cuh
+
+
+def _here(dev, stream):
+    return stream is None and dev.index is not None and dev.index == _current_device()
+
+
+def kda_gated_scan_prefill(x, gate, *, gate_kind="log", input_kind="plain", cu_seqlens=None, cu_seqlens_host=None,
+                           num_seqs=None, state_in=None, state_out=None, o=None, state_slots=None, schedule="auto",
+                           workspace=True, stream=None):
+    """The recurrence of one number per channel over packed sequences
+    (kda_gated_scan_prefill): h <- a h + b x, o = h per token.
+
+    x, gate, o: [T, C] (bf16 or fp32, one dtype; C a multiple of 8, tokens at any stride of
+    whole 16 bytes).  gate_kind "log": a = exp(min(gate, 0)); "sigmoid": the logistic
+    function of it.  input_kind "plain": b = 1; "complement": 1 - a; "norm": sqrt(1 - a^2).
+    The state is [N, C] fp32, or bf16 storage when those tensors are bf16; with
+    state_slots (int32 [N]) the state tensors are pools and sequence n uses row
+    state_slots[n].  state_out: a tensor, or True to allocate one of state_in's dtype
+    (else fp32).  schedule: "auto", "one_pass" or "chained" (include/kda.h).  workspace:
+    True allocates what the schedule needs, a uint8 tensor is used, None or False gives
+    none (one pass).  Returns (o, state_out)."""
+    lib = _lib or load_library()
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2:
+        raise ValueError("x must be [T, C], got %s" % (tuple(x.shape),))
+    T, C = shape = x.shape
+    gk, ik = _kinds(gate_kind, input_kind)
+    sched = _scan_schedule(schedule)
+    xs = _rows2(x, "x", shape, dt, dev)
+    gs = _rows2(gate, "gate", shape, dt, dev)
+    N, cup, cuh = _cu(cu_seqlens, cu_seqlens_host, num_seqs, dev)
+    given = torch.is_tensor(state_out)
+    sdt = state_in.dtype if state_in is not None else state_out.dtype if given else torch.float32
+    flags = slots = num_slots = sip = sop = os_ = 0
+    if state_slots is not None:
+        if not given and (state_out or state_in is None):
+            raise ValueError("with state_slots, pass the pool tensors as state_in / state_out")
+        for t, nm in ((state_in, "state_in"), (state_out, "state_out")):
+            _pool_shape(t, nm, (C,))
+        _, num_slots = _slots(state_slots, (state_in, state_out), N, dev)
+        slots = state_slots.data_ptr()
+    if state_in is not None:
+        _need(state_in, "state_in", None, dev)
+        if slots == 0:
+            _shape(state_in, "state_in", (N, C))
+        flags = _state_flag(state_in)
+        sip = state_in.data_ptr()
+    if given:
+        _need(state_out, "state_out", None, dev)
+        if slots == 0:
+            _shape(state_out, "state_out", (N, C))
+        if state_out.dtype is not sdt:
+            raise TypeError("state_in and state_out must have one dtype")
+        flags = _state_flag(state_out)
+    if o is not None:
+        os_ = _rows2(o, "o", shape, dt, dev)
+    if torch.is_tensor(workspace):
+        _need(workspace, "workspace", torch.uint8, dev)
+    code = _io_code(dt)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return kda_gated_scan_prefill(
+                x, gate, gate_kind=gate_kind, input_kind=input_kind, cu_seqlens=cu_seqlens, cu_seqlens_host=cuh,
+                num_seqs=num_seqs, state_in=state_in, state_out=state_out, o=o, state_slots=state_slots,
+                schedule=schedule, workspace=workspace)
+    if o is None:
+        o = torch.empty_like(x, memory_format=_dense)
+    if state_out is True:
+        state_out = torch.empty((N, C), dtype=sdt, device=dev)
+    elif state_out is False:
+        state_out = None
+    if state_out is not None:
+        sop = state_out.data_ptr()
+
+    def args(ws, size):
+        return _SCAN_PACK.pack(
+            N, C, T, code, gk, ik, flags, xs, gs, os_, x.data_ptr(), gate.data_ptr(), sip, sop, o.data_ptr(), cup,
+            0 if cuh is None else cuh.data_ptr(), slots, num_slots, sched, ws, size)
+
+    st = lib.kda_gated_scan_prefill(_with_workspace(lib.kda_gated_scan_workspace_size, args, workspace, dev),
+                                    _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
+    return o, state_out
+
+
+def _with_workspace(size_of, args, workspace, dev):
+    """Packed arguments with the workspace that the caller gave or that the call needs.
+    (An allocated one is freed on return: the allocator hands its memory on only to later
+    work of the same stream.)"""
+    if workspace is True:
+        need = size_of(args(0, 0))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if torch.is_tensor(workspace):
+        return args(workspace.data_ptr(), workspace.numel())
+    return args(0, 0)
+
+
+def kda_gated_scan_decode(x, gate, state, *, gate_kind="log", input_kind="plain", o=None, state_slots=None, stream=None):
+    """One token of the gated scan for each of N sequences (kda_gated_scan_decode): x, gate
+    [N, C]; state [N, C] (fp32, or bf16 storage), or a pool with state_slots, is updated in
+    place.  Kinds, strides and types as in kda_gated_scan_prefill.  Returns o [N, C]."""
+    lib = _lib or load_library()
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C], got %s" % (tuple(x.shape),))
+    N, C = shape = x.shape
+    gk, ik = _kinds(gate_kind, input_kind)
+    xs = _rows2(x, "x", shape, dt, dev)
+    gs = _rows2(gate, "gate", shape, dt, dev)
+    flags = _state_flag(state)
+    _need(state, "state", None, dev)
+    slots = num_slots = os_ = 0
+    if state_slots is not None or state.shape != shape:
+        _pool_shape(state, "state", (C,))
+        _, num_slots = _slots(state_slots, (state,), N, dev)
+        slots = state_slots.data_ptr()
+    if o is not None:
+        os_ = _rows2(o, "o", shape, dt, dev)
+    code = _io_code(dt)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return kda_gated_scan_decode(x, gate, state, gate_kind=gate_kind, input_kind=input_kind, o=o,
+                                         state_slots=state_slots)
+    if o is None:
+        o = torch.empty_like(x, memory_format=_dense)
+    st = lib.kda_gated_scan_decode(
+        _STEP_PACK.pack(N, C, code, gk, ik, flags, xs, gs, os_, x.data_ptr(), gate.data_ptr(), state.data_ptr(),
+                        o.data_ptr(), slots, num_slots), _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
+    return o
+
+
+def kda_gated_scan_backward(d_o, gate, o, x=None, *, gate_kind="log", input_kind="plain", cu_seqlens=None,
+                            cu_seqlens_host=None, num_seqs=None, state_in=None, dstate_out=None, dx=None, dgate=None,
+                            dstate_in=None, schedule="auto", workspace=True, stream=None):
+    """Gradients of kda_gated_scan_prefill (kda_gated_scan_backward) from d_o [T, C], that of
+    o, and dstate_out [N, C] fp32, that of the final state (None: zeros).  gate, o and
+    state_in are the forward call's (its output o holds the states); x too, which
+    input_kind "plain" does not take.  dx, dgate: [T, C], allocated when not given;
+    dstate_in: fp32 [N, C], or True to allocate it; it may be dstate_out.  In bf16 the
+    states are those that o holds, rounded once.  Returns (dx, dgate, dstate_in)."""
+    lib = _lib or load_library()
+    dev, dt = d_o.device, d_o.dtype
+    if d_o.dim() != 2:
+        raise ValueError("d_o must be [T, C], got %s" % (tuple(d_o.shape),))
+    T, C = shape = d_o.shape
+    gk, ik = _kinds(gate_kind, input_kind)
+    sched = _scan_schedule(schedule)
+    ds = _rows2(d_o, "d_o", shape, dt, dev)
+    gs = _rows2(gate, "gate", shape, dt, dev)
+    os_ = _rows2(o, "o", shape, dt, dev)
+    if (x is None) != (ik == 0):
+        raise ValueError("x goes with input_kind 'complement' and 'norm', and only with them")
+    xs = xp = dxs = dgs = flags = 0
+    if x is not None:
+        xs, xp = _rows2(x, "x", shape, dt, dev), x.data_ptr()
+    N, cup, cuh = _cu(cu_seqlens, cu_seqlens_host, num_seqs, dev)
+    _need(state_in, "state_in", None, dev)
+    _shape(state_in, "state_in", (N, C))
+    if state_in is not None:
+        flags = _state_flag(state_in)
+    _need(dstate_out, "dstate_out", torch.float32, dev)
+    _shape(dstate_out, "dstate_out", (N, C))
+    if torch.is_tensor(dstate_in):
+        _need(dstate_in, "dstate_in", torch.float32, dev)
+        _shape(dstate_in, "dstate_in", (N, C))
+    if dx is not None:
+        dxs = _rows2(dx, "dx", shape, dt, dev)
+    if dgate is not None:
+        dgs = _rows2(dgate, "dgate", shape, dt, dev)
+    if torch.is_tensor(workspace):
+        _need(workspace, "workspace", torch.uint8, dev)
+    code = _io_code(dt)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return kda_gated_scan_backward(
+                d_o, gate, o, x, gate_kind=gate_kind, input_kind=input_kind, cu_seqlens=cu_seqlens,
+                cu_seqlens_host=cuh, num_seqs=num_seqs, state_in=state_in, dstate_out=dstate_out, dx=dx, dgate=dgate,
+                dstate_in=dstate_in, schedule=schedule, workspace=workspace)
+    if dx is None:
+        dx = torch.empty_like(d_o, memory_format=_dense)
+    if dgate is None:
+        dgate = torch.empty_like(d_o, memory_format=_dense)
+    if dstate_in is True:
+        dstate_in = torch.empty((N, C), dtype=torch.float32, device=dev)
+    elif dstate_in is False:
+        dstate_in = None
+
+    def args(ws, size):
+        return _SCAN_GRAD_PACK.pack(
+            N, C, T, code, gk, ik, flags, ds, gs, os_, xs, dxs, dgs, d_o.data_ptr(), gate.data_ptr(), o.data_ptr(), xp,
+            0 if state_in is None else state_in.data_ptr(), 0 if dstate_out is None else dstate_out.data_ptr(),
+            dx.data_ptr(), dgate.data_ptr(), 0 if dstate_in is None else dstate_in.data_ptr(), cup,
+            0 if cuh is None else cuh.data_ptr(), sched, ws, size)
+
+    st = lib.kda_gated_scan_backward(_with_workspace(lib.kda_gated_scan_backward_workspace_size, args, workspace, dev),
+                                     _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
+    return dx, dgate, dstate_in
+
+
+def kda_add_norm(x, residual=None, weight=None, *, eps=1e-6, quant="none", residual_out=None, y=None, scale=None,
+                 stream=None):
+    """Residual addition and RMS norm of whole rows, with an output in 8 bits if asked for
+    (kda_add_norm): s = x + residual, y = weight * s / rms(s).
+
+    x, residual: [T, C] (bf16 or fp32; C a multiple of 8 up to 16384, tokens at any stride
+    of whole 16 bytes); weight fp32 [C] or None.  quant "none": y in x's dtype; "token" and
+    "group": y / scale as float8_e4m3fn with fp32 scales [T], or [T, C / 128] (C a multiple
+    of 128).  residual_out gets s in x's dtype: a tensor (x or residual in place), None to
+    allocate one where a residual is given, False for none.  Returns (y, scale, residual_out),
+    None where there is none."""
+    lib = _lib or load_library()
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if x.dim() != 2:
+        raise ValueError("x must be [T, C], got %s" % (tuple(shape),))
+    T, C = shape
+    qk = QUANTS.get(quant)
+    if qk is None:
+        raise ValueError("quant must be one of %s" % sorted(QUANTS))
+    xs = _rows2(x, "x", shape, dt, dev)
+    rs = ss = ys = rp = wp = 0
+    if residual is not None:
+        rs, rp = _rows2(residual, "residual", shape, dt, dev), residual.data_ptr()
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev)
+        _shape(weight, "weight", (C,))
+        wp = weight.data_ptr()
+    if torch.is_tensor(residual_out):
+        ss = _rows2(residual_out, "residual_out", shape, dt, dev)
+    ydt = dt if qk == 0 else torch.float8_e4m3fn
+    if y is not None:
+        ys = _rows2(y, "y", shape, ydt, dev)
+    if qk == 2 and C % 128:
+        raise ValueError("quant 'group' needs channels in multiples of 128, got %d" % C)
+    sshape = (T,) if qk == 1 else (T, C // 128)
+    if scale is not None:
+        if qk == 0:
+            raise ValueError("scale goes with quant 'token' and 'group'")
+        _need(scale, "scale", torch.float32, dev)
+        _shape(scale, "scale", sshape)
+    code = _io_code(dt)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return kda_add_norm(x, residual, weight, eps=eps, quant=quant, residual_out=residual_out, y=y, scale=scale)
+    if residual_out is None and residual is not None or residual_out is True:
+        residual_out = torch.empty_like(x, memory_format=_dense)
+    elif residual_out is False:
+        residual_out = None
+    if y is None:
+        y = torch.empty_like(x, dtype=ydt, memory_format=_dense)
+    if scale is None and qk:
+        scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+    st = lib.kda_add_norm(
+        _ADD_NORM_PACK.pack(T, C, code, qk, eps, xs, rs, ss, ys, x.data_ptr(), rp, wp,
+                            0 if residual_out is None else residual_out.data_ptr(), y.data_ptr(),
+                            0 if scale is None else scale.data_ptr()), _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
+    return y, scale, residual_out
+
+
+def kda_add_norm_backward(dy, s, weight=None, *, eps=1e-6, dresidual=None, dx=None, dweight=True, workspace=True,
+                          stream=None):
+    """Gradients of kda_add_norm (kda_add_norm_backward) from dy, that of y before any
+    rounding to 8 bits, and dresidual, that of residual_out (None: none).  s is the forward
+    call's residual_out (x where it had no residual); all [T, C], one dtype.  dx is the
+    gradient of x and of residual alike, and may be dy, s or dresidual; dweight: fp32 [C],
+    True to allocate it, None or False for none.  Returns (dx, dweight)."""
+    lib = _lib or load_library()
+    dev, dt, shape = dy.device, dy.dtype, dy.shape
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, C], got %s" % (tuple(shape),))
+    T, C = shape
+    ys = _rows2(dy, "dy", shape, dt, dev)
+    ss = _rows2(s, "s", shape, dt, dev)
+    rs = xs = rp = wp = 0
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev)
+        _shape(weight, "weight", (C,))
+        wp = weight.data_ptr()
+    if dresidual is not None:
+        rs, rp = _rows2(dresidual, "dresidual", shape, dt, dev), dresidual.data_ptr()
+    if dx is not None:
+        xs = _rows2(dx, "dx", shape, dt, dev)
+    if torch.is_tensor(dweight):
+        _need(dweight, "dweight", torch.float32, dev)
+        _shape(dweight, "dweight", (C,))
+    if torch.is_tensor(workspace):
+        _need(workspace, "workspace", torch.uint8, dev)
+    code = _io_code(dt)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return kda_add_norm_backward(dy, s, weight, eps=eps, dresidual=dresidual, dx=dx, dweight=dweight,
+                                         workspace=workspace)
+    if dx is None:
+        dx = torch.empty_like(dy, memory_format=_dense)
+    if dweight is True:
+        dweight = torch.empty((C,), dtype=torch.float32, device=dev)
+    elif dweight is False:
+        dweight = None
+
+    def args(ws, size):
+        return _ADD_NORM_GRAD_PACK.pack(T, C, code, eps, ys, ss, rs, xs, dy.data_ptr(), s.data_ptr(), rp, wp,
+                                        dx.data_ptr(), 0 if dweight is None else dweight.data_ptr(), ws, size)
+
+    st = lib.kda_add_norm_backward(_with_workspace(lib.kda_add_norm_backward_workspace_size, args, workspace, dev),
+                                   _raw_stream(dev.index))
+    if st:
+        _check(lib, st)
+    return dx, dweight
 
 
 # ------------------------------------------------------------------ calibration

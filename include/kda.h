@@ -206,6 +206,7 @@ typedef enum {
     KDA_SCHEDULE_ONE_PASS = 1,
     KDA_SCHEDULE_TWO_PASS = 2,
     KDA_SCHEDULE_FUSED = 3,
+    KDA_SCHEDULE_CHAINED = 4,  /* the gated scan only */
 } kda_schedule;
 
 /* The automatic choice takes the fused schedule from this many (sequence, head)
@@ -646,6 +647,178 @@ typedef struct {
 } kda_gated_norm_args;
 
 kda_status kda_gated_norm(const kda_gated_norm_args *args, hipStream_t stream);
+
+/*
+ * Gated scan: the recurrence of one number per channel, for layers whose state is a
+ * vector (beside the matrix states above; kda_short_conv stands before it in such a
+ * layer, kda_gated_norm behind it).  Per token t of a sequence and channel, with the
+ * gate value z_t:
+ *     h_t = a_t h_{t-1} + b_t x_t,      o_t = h_t
+ *     a = exp(min(z, 0))     KDA_GATE_LOG      (z is the log-decay)
+ *     a = 1 / (1 + exp(-z))  KDA_GATE_SIGMOID  (z is a pre-activation)
+ *     b = 1                  KDA_INPUT_PLAIN
+ *     b = 1 - a              KDA_INPUT_COMPLEMENT
+ *     b = sqrt(1 - a^2)      KDA_INPUT_NORM    (keeps the state's variance)
+ * Layouts: x, gate and o [T][C] in `dtype`, C a multiple of 8, each with a stride from
+ * one token to the next (0 = dense; views of a packed projection), 16-byte aligned.
+ * State [N][C], fp32 or bf16 with KDA_F_STATE_BF16; state_slots works as in "State pool"
+ * above.  States, decays and 1 - a are formed and carried in fp32, decays as sums of
+ * logarithms, and 1 - a without the cancellation: long memories keep their length.  o, and
+ * a bf16 state, are rounded once.  A non-finite x, gate or state reaches later tokens of
+ * its own sequence and channel and nothing else; an infinity in a state may become NaN
+ * once the decays behind it multiply to less than 2^-126.
+ */
+typedef enum { KDA_GATE_LOG = 0, KDA_GATE_SIGMOID = 1 } kda_gate_kind;
+typedef enum { KDA_INPUT_PLAIN = 0, KDA_INPUT_COMPLEMENT = 1, KDA_INPUT_NORM = 2 } kda_input_kind;
+
+typedef struct {
+    int32_t num_seqs;        /* N >= 1 */
+    int32_t channels;        /* C: a positive multiple of 8 */
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    kda_dtype dtype;
+    kda_gate_kind gate_kind;
+    kda_input_kind input_kind;
+    uint32_t flags;          /* 0 or KDA_F_STATE_BF16 */
+    int64_t x_stride, gate_stride, o_stride; /* elements per token, 0 = dense */
+    const void *x, *gate;    /* [T][C] */
+    const void *state_in;    /* [N][C] or NULL (zeros) */
+    void *state_out;         /* [N][C] or NULL; may alias state_in */
+    void *o;                 /* [T][C]; must not overlap the inputs */
+    const int32_t *cu_seqlens;      /* [N+1] device, or NULL for N equal sequences */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated when given */
+    const int32_t *state_slots;     /* [N] device pool slots, or NULL */
+    int32_t num_slots;              /* pool rows when state_slots is given */
+    int32_t schedule;               /* KDA_SCHEDULE_AUTO, _ONE_PASS or _CHAINED */
+    void *workspace;                /* device scratch of the chained schedule, or NULL */
+    size_t workspace_bytes;         /* its size; see kda_gated_scan_workspace_size */
+} kda_gated_scan_args;
+
+/* Packed prompts, every sequence from its initial state to its final one; empty
+ * sequences pass their state through.  Two schedules (same results, bit for bit):
+ *   - one pass: a workgroup walks a sequence, 128 channels wide; no workspace;
+ *   - chained: workgroups take tiles of a sequence side by side and hand the state from
+ *     tile to tile through the workspace, after a launch that clears it.  A tile waits
+ *     only for tiles that run or have run, so every wait ends; kda_set_spin_limit bounds
+ *     it all the same, and a wait that gives up makes its outputs NaN.
+ * KDA_SCHEDULE_AUTO takes the faster one where a workspace is given, by the longest
+ * sequence that cu_seqlens_host (or equal sequences) shows, else by T.  The workspace is
+ * overwritten by each call and must not be shared by calls that may overlap in time. */
+kda_status kda_gated_scan_prefill(const kda_gated_scan_args *args, hipStream_t stream);
+
+/* Workspace bytes of the schedule that a call runs when it is given one (0: one pass).
+ * Depends on num_seqs, channels, total_tokens, dtype, schedule, cu_seqlens_host and
+ * whether cu_seqlens is given. */
+size_t kda_gated_scan_workspace_size(const kda_gated_scan_args *args);
+
+typedef struct {
+    int32_t num_seqs;        /* N >= 1: one token each */
+    int32_t channels;        /* C: a positive multiple of 8 */
+    kda_dtype dtype;
+    kda_gate_kind gate_kind;
+    kda_input_kind input_kind;
+    uint32_t flags;          /* 0 or KDA_F_STATE_BF16 */
+    int64_t x_stride, gate_stride, o_stride; /* elements per sequence, 0 = dense */
+    const void *x, *gate;    /* [N][C] */
+    void *state;             /* [N][C] in/out: the layout prefill writes */
+    void *o;                 /* [N][C]; must not overlap the inputs */
+    const int32_t *state_slots;
+    int32_t num_slots;
+} kda_gated_scan_decode_args;
+
+/* One new token for each of N sequences, the states updated in place. */
+kda_status kda_gated_scan_decode(const kda_gated_scan_decode_args *args, hipStream_t stream);
+
+/* The gradients of kda_gated_scan_prefill from those of o and of the final state:
+ *     r_T = dstate_out,  dh_t = d_o_t + r_t,  r_{t-1} = a_t dh_t,  dstate_in = r_0
+ *     dx_t = b_t dh_t,   dgate_t = dh_t (h_{t-1} da/dz + x_t db/dz)
+ * with h_{t-1} read from the forward pass's o (and state_in before the first token): in
+ * bf16 as it was rounded there.  A log-decay above 0 has no gradient; KDA_INPUT_NORM's
+ * db/dz, infinite where a reaches 1, counts as 0 where b is 0.  dstate_out and dstate_in
+ * are fp32.  States are not pooled here: sequence n owns row n. */
+typedef struct {
+    int32_t num_seqs;        /* N >= 1 */
+    int32_t channels;        /* C: a positive multiple of 8 */
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    kda_dtype dtype;
+    kda_gate_kind gate_kind;
+    kda_input_kind input_kind;
+    uint32_t flags;          /* 0 or KDA_F_STATE_BF16 (state_in) */
+    int64_t d_o_stride, gate_stride, o_stride, x_stride, dx_stride, dgate_stride;
+    const void *d_o;         /* [T][C] gradient of o */
+    const void *gate, *o;    /* [T][C], as in the forward call */
+    const void *x;           /* [T][C]; NULL exactly with KDA_INPUT_PLAIN */
+    const void *state_in;    /* [N][C] as in the forward call, or NULL (zeros) */
+    const float *dstate_out; /* [N][C] gradient of the final state, or NULL (zeros) */
+    void *dx, *dgate;        /* [T][C]; must not overlap the inputs */
+    float *dstate_in;        /* [N][C] gradient of state_in, or NULL; may alias dstate_out */
+    const int32_t *cu_seqlens;      /* [N+1] device, or NULL for N equal sequences */
+    const int32_t *cu_seqlens_host; /* optional host copy, validated when given */
+    int32_t schedule;               /* KDA_SCHEDULE_AUTO, _ONE_PASS or _CHAINED */
+    void *workspace;
+    size_t workspace_bytes;         /* see kda_gated_scan_backward_workspace_size */
+} kda_gated_scan_backward_args;
+
+kda_status kda_gated_scan_backward(const kda_gated_scan_backward_args *args, hipStream_t stream);
+size_t kda_gated_scan_backward_workspace_size(const kda_gated_scan_backward_args *args);
+
+/*
+ * kda_add_norm -- the norm in front of a layer's in-projections: the residual's addition,
+ * the RMS norm over the whole row and, if asked for, the output in 8 bits with scales.
+ * Per token, of C channels:
+ *     s = x + residual                      (x where residual is NULL)
+ *     y = w * s / sqrt(|s|^2 / C + eps)     (w of C fp32, NULL = 1)
+ * KDA_QUANT_NONE writes y in `dtype`.  KDA_QUANT_TOKEN and KDA_QUANT_GROUP write y / scale
+ * as e4m3 (largest value 448, round to nearest even) and the fp32 scales, one for each
+ * token or for each 128 channels of it: scale = max|y| / 448, at least 2^-126, and 1 where
+ * the maximum is 0.  A non-finite scale is NaN, and so is every value under it.  s is formed
+ * and normalised in fp32 (the squares of a row have to stay in its range: |s| below about
+ * 1e17); residual_out gets it in `dtype` and may be x or residual (same pointer and stride).
+ * Bases and token strides are whole 16 bytes, of an 8-bit y whole 8 bytes.
+ */
+typedef enum { KDA_QUANT_NONE = 0, KDA_QUANT_TOKEN = 1, KDA_QUANT_GROUP = 2 } kda_quant;
+#define KDA_ADD_NORM_MAX_CHANNELS 16384
+
+typedef struct {
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int32_t channels;        /* C: a multiple of 8 (of 128 with KDA_QUANT_GROUP), up to
+                                KDA_ADD_NORM_MAX_CHANNELS */
+    kda_dtype dtype;         /* of x, residual, residual_out and an unquantised y */
+    kda_quant quant;
+    float eps;               /* > 0 */
+    int64_t x_stride, residual_stride, residual_out_stride, y_stride; /* elements per token, 0 = dense */
+    const void *x;           /* [T][C] */
+    const void *residual;    /* [T][C] or NULL */
+    const float *weight;     /* [C] or NULL */
+    void *residual_out;      /* [T][C] or NULL */
+    void *y;                 /* [T][C]: dtype, or one byte each */
+    float *scale;            /* [T] or [T][C / 128]; NULL exactly with KDA_QUANT_NONE */
+} kda_add_norm_args;
+
+kda_status kda_add_norm(const kda_add_norm_args *args, hipStream_t stream);
+
+/* The gradients of kda_add_norm from that of y (as it was before any rounding to 8 bits)
+ * and, optionally, of residual_out.  With n = s / rms(s), per token
+ *     dx = (w dy - n mean(w dy n)) / rms(s) + dresidual
+ * is the gradient of s, hence of x and of residual alike, and dweight = sum over tokens of
+ * dy n.  s is the forward call's residual_out.  dx may be dy, s or dresidual (same pointer
+ * and stride).  The sums of dweight run in a fixed order through the workspace. */
+typedef struct {
+    int64_t total_tokens;
+    int32_t channels;        /* C: a multiple of 8, up to KDA_ADD_NORM_MAX_CHANNELS */
+    kda_dtype dtype;         /* of dy, s, dresidual and dx */
+    float eps;               /* > 0 */
+    int64_t dy_stride, s_stride, dresidual_stride, dx_stride; /* elements per token, 0 = dense */
+    const void *dy, *s;      /* [T][C] */
+    const void *dresidual;   /* [T][C] or NULL */
+    const float *weight;     /* [C] or NULL */
+    void *dx;                /* [T][C] */
+    float *dweight;          /* [C] or NULL */
+    void *workspace;         /* device scratch, needed with dweight */
+    size_t workspace_bytes;  /* its size; see kda_add_norm_backward_workspace_size */
+} kda_add_norm_backward_args;
+
+kda_status kda_add_norm_backward(const kda_add_norm_backward_args *args, hipStream_t stream);
+size_t kda_add_norm_backward_workspace_size(const kda_add_norm_backward_args *args);
 
 #ifdef __cplusplus
 }
