@@ -3,19 +3,21 @@
 //
 // The recurrence is linear in the state, so a run of tokens acts on the state before it
 // as one step (P, H): h -> P h + H, and runs are joined by (P2 P1, P2 H1 + H2).  A tile
-// is kRows tokens x kWaves waves of 128 channels: a lane owns two neighbouring channels
-// and a wave kRows tokens of them.  In a tile
-//   1. each wave forms its rows' step from its last row to its first,
-//      H = sum_t exp2(l_{t+1} + .. + l_last) u_t,  log2 P = sum l_t, with l = log2 a and
-//      u = b x, all rows independent but for a running sum of l;
-//   2. the waves' steps are joined through LDS with the state before the tile;
-//   3. each wave runs the recurrence over its rows from its own first state.
-// Decays are summed as logarithms over a tile, so a decay near 1 loses nothing to the
-// rounding of a = 1 - small: that error would grow with the length of the memory.
+// is S tokens x 7 or 15 waves of 128 channels: a lane owns two neighbouring channels and a
+// wave S tokens of them.  For each tile
+//   1. every wave forms its rows' step and leaves it in LDS;
+//   2. the manager, a wave of its own without rows, joins the steps, finds the state
+//      before the tile and leaves each wave the state that it begins from.  Meanwhile the
+//      others send for the rows of the next tile, which the manager has found before;
+//   3. every wave runs the recurrence over its rows and writes them.
+// Between tiles decays are handed on as logarithms, and only a whole tile's is rounded as
+// a decay: the rounding of every a = 1 - small, the same for every token of a steady
+// gate, would grow with the length of the memory.
 //
-// One pass: a workgroup walks the tiles of one (sequence, 128 channels).  Chained: a
-// workgroup takes one tile and waits for the state before it (see chain_carry).  Either
-// way every element is read once and written once: the bound is HBM.
+// One pass: a workgroup walks the tiles of one (sequence, 128 channels), the manager keeps
+// the state.  Chained: a workgroup takes tiles by ticket, and the state comes from the
+// workgroup before it through the workspace (chain_carry).  Either way every element is
+// read once and written once: the bound is HBM.
 #include <algorithm>
 
 #include "kda_scan.h"
@@ -24,208 +26,292 @@ namespace kda {
 
 namespace {
 
-// From the state `h` before the tile: the state before chain position `pos`, and in h the
-// one behind the tile (the whole tile's decay rounded once, as chain_carry does).
-template <int WAVES>
-__device__ __forceinline__ void join(const float4 (*steps)[64], int lane, int pos, float2 &h, float2 &mine) {
-    float2 sum = {0.f, 0.f}, add = {0.f, 0.f};
+template <int WAVES> struct Shared {
+    Tile tile[2];             // of iterations i (i & 1)
+    float4 steps[WAVES][64];  // from the waves: log2 P and H; to them: P and H of the rows before theirs
+    float2 carry[64];         // the state before the tile
+};
+
+// The manager's part.  `edge` is where a sequence's chain begins: its first tile, or for
+// the gradients its last.  `first` and `final` are the states there and at the other end.
+template <int TILE, bool BACKWARD, bool CHAINED, int WAVES, typename First, typename Final>
+__device__ __forceinline__ void manage(const ScanParams &p, Shared<WAVES> &sh, int lane, First first, Final final) {
+    const uint32_t taken = CHAINED ? take_ticket(p, lane) : 0;
+    const Sequences seq(p, lane);
+    float2 running = {0.f, 0.f};
+    auto next = [&](const Tile &before) __attribute__((always_inline)) {
+        Tile t = before;
+        if (before.n >= 0) {  // one pass: the sequence goes on, or ends
+            t.index += BACKWARD ? -1 : 1;
+            if (CHAINED || t.index < 0 || t.index >= t.count) t.n = -1;
+            return t;
+        }
+        if (CHAINED) {
+            t = ticket_tile<TILE, BACKWARD>(p, seq, taken);
+        } else {
+            t.m = blockIdx.x / p.groups;
+            t.group = blockIdx.x - t.m * p.groups;
+            seq.fill<TILE>(t.m, t);
+            t.index = BACKWARD ? t.count - 1 : 0;
+        }
+        if (t.slot < 0) t.n = -1;
+        if (t.n >= 0 && t.count == 0) {  // no tokens: the state is passed on
+            final(t, first(t));
+            t.n = -1;
+        }
+        return t;
+    };
+    Tile cur = {};
+    cur.n = -1;
+    cur = next(cur);
+    if (lane == 0) sh.tile[0] = cur;
+    barrier_lds();
+    for (int i = 1; cur.n >= 0; ++i) {
+        const int edge = BACKWARD ? cur.count - 1 : 0, done = BACKWARD ? edge - cur.index : cur.index;
+        float2 h = done == 0 ? first(cur) : running;
+        const Tile after = next(cur);
+        if (lane == 0) sh.tile[i & 1] = after;
+        barrier_lds();
+        float2 sum = {0.f, 0.f}, add = {0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < WAVES; ++q) {
-        if (q == pos) mine = make_float2(fmaf(exp2_fast(sum.x), h.x, add.x), fmaf(exp2_fast(sum.y), h.y, add.y));
-        append(steps[q][lane], sum, add);
+        for (int q = 0; q < WAVES; ++q) {
+            const float4 s = sh.steps[q][lane];
+            sh.steps[q][lane] = make_float4(exp2_fast(sum.x), exp2_fast(sum.y), add.x, add.y);
+            sum.x += s.x;
+            sum.y += s.y;
+            add.x = fmaf(exp2_fast(s.x), add.x, s.z);
+            add.y = fmaf(exp2_fast(s.y), add.y, s.w);
+        }
+        const float2 dec = {exp2_fast(sum.x), exp2_fast(sum.y)};
+        if (CHAINED) h = chain_carry(p, cur, lane, done, BACKWARD ? 1 : -1, dec, add, h);
+        sh.carry[lane] = h;
+        barrier_lds();
+        running = make_float2(fmaf(dec.x, h.x, add.x), fmaf(dec.y, h.y, add.y));
+        if (done == cur.count - 1) final(cur, running);
+        cur = after;
     }
-    h = make_float2(fmaf(exp2_fast(sum.x), h.x, add.x), fmaf(exp2_fast(sum.y), h.y, add.y));
 }
 
-template <typename T, int GATE, int INPUT, bool CHAINED>
-__global__ void __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 4 : 2) scan_kernel(ScanParams p) {
-    typedef typename Pair<T>::vec vec;
-    constexpr int S = kRows, TILE = S * kWaves;
-    __shared__ float4 steps[2][kWaves][64];
-    __shared__ float2 carry[64];
-    __shared__ TileId shared_id;
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const TileId id = CHAINED ? chained_tile<TILE>(p, wave, lane, &shared_id, false) : whole_sequence(p);
-    if (id.n < 0) return;
-    const int slot = pool_slot(p.slots, p.num_slots, id.n);
-    if (slot < 0) return;
-    const int c = id.group * 128 + 2 * lane;
-    const bool on = c < p.C;
-    const int cl = on ? c : p.C - 2;
-    const size_t srow = (size_t)slot * p.C + cl;
-    const int tiles = (int)((id.len + TILE - 1) / TILE);
+// The state that the rows at chain position `pos` begin from.
+template <int WAVES> __device__ __forceinline__ float2 begin_state(const Shared<WAVES> &sh, int lane, int pos) {
+    const float4 s = sh.steps[pos][lane];
+    const float2 c = sh.carry[lane];
+    return make_float2(fmaf(s.x, c.x, s.z), fmaf(s.y, c.y, s.w));
+}
 
-    vec rx[S], rg[S];
-    auto load = [&](int i) __attribute__((always_inline)) {
-        const int64_t t0 = (int64_t)i * TILE + wave * S;
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-            const int64_t t = id.start + min(t0 + j, id.len - 1);
-            rx[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.x) + t * p.xs + cl);
-            rg[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.g) + t * p.gs + cl);
-        }
-    };
-    float2 h = {0.f, 0.f};
-    const int first = CHAINED ? id.index : 0, end = CHAINED ? min(id.index + 1, tiles) : tiles;
-    if (first < end) load(first);
-    if (p.state_in && first == 0) h = load_state(p.state_in, srow, p.state_bf16);
-    for (int i = first; i < end; ++i) {
-        const int64_t t0 = (int64_t)i * TILE + wave * S;
-        float l[S][2], u[S][2];
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-            const bool in = t0 + j < id.len;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const Factors<GATE, INPUT> f(to_f32(rg[j][v]));
-                l[j][v] = in ? f.l : 0.f;
-                u[j][v] = in ? f.input(to_f32(rx[j][v])) : 0.f;
-            }
-        }
-        if (!CHAINED && i + 1 < end) load(i + 1);
-        float sum[2] = {0.f, 0.f}, add[2] = {u[S - 1][0], u[S - 1][1]};
-#pragma unroll
-        for (int j = S - 1; j >= 0; --j)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                if (j < S - 1) add[v] = fmaf(u[j][v], exp2_fast(sum[v]), add[v]);
-                sum[v] += l[j][v];
-            }
-        float4(*st)[64] = steps[CHAINED ? 0 : i & 1];
-        st[wave][lane] = make_float4(sum[0], sum[1], add[0], add[1]);
-        __syncthreads();
-        float2 mine = {0.f, 0.f};
-        if (CHAINED) {
-            if (wave == 0) {
-                const float2 before = chain_carry<kWaves>(p, id, lane, 0, tiles, st, h);
-                carry[lane] = before;
-                float2 after = before;
-                if (i == tiles - 1 && p.state_out) {
-                    join<kWaves>(st, lane, 0, after, mine);
-                    if (on) store_state(p.state_out, srow, p.state_bf16, after);
-                }
-            }
-            __syncthreads();
-            h = carry[lane];
-        }
-        join<kWaves>(st, lane, wave, h, mine);
-        T *o = static_cast<T *>(p.o) + (id.start + t0) * p.os + cl;
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-            mine.x = fmaf(exp2_fast(l[j][0]), mine.x, u[j][0]);
-            mine.y = fmaf(exp2_fast(l[j][1]), mine.y, u[j][1]);
-            if (t0 + j < id.len && on) Pair<T>::store(o + j * p.os, mine.x, mine.y);
-        }
+// Byte offset of a lane's channels in a row; past every buffer where there are none.
+template <typename T> __device__ __forceinline__ uint32_t lane_offset(const ScanParams &p, const Tile &t, int lane) {
+    const int c = t.group * 128 + 2 * lane;
+    return c < p.C ? (uint32_t)c * sizeof(T) : RowBuffer<T>::kNowhere;
+}
+
+// Rows whose factors are formed side by side: more would not fit the registers.
+constexpr int kTogether = 2;
+
+template <typename T, int GATE, int INPUT, bool CHAINED>
+__global__ void __launch_bounds__(64 * (scan_waves(CHAINED) + 1), scan_occupancy(sizeof(T), false, scan_cheap(GATE, INPUT))) scan_kernel(ScanParams p) {
+    typedef Two<T> two;
+    constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), false, CHEAP);
+    constexpr int WAVES = scan_waves(CHAINED), S = scan_rows(sizeof(T), false, GATE, INPUT), TILE = S * WAVES;
+    __shared__ Shared<WAVES> sh;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if (wave == WAVES) {
+        auto at = [&](const Tile &t) { return (size_t)t.slot * p.C + t.group * 128 + 2 * lane; };
+        auto on = [&](const Tile &t) { return t.group * 128 + 2 * lane < p.C; };
+        manage<TILE, false, CHAINED, WAVES>(
+            p, sh, lane,
+            [&](const Tile &t) { return p.state_in && on(t) ? load_state(p.state_in, at(t), p.state_bf16) : float2{0.f, 0.f}; },
+            [&](const Tile &t, float2 h) { if (p.state_out && on(t)) store_state(p.state_out, at(t), p.state_bf16, h); });
+        return;
     }
-    // (a chained tile's state went out with its carry; a sequence without tokens passes its own on)
-    if (p.state_out && on && wave == 0 && (!CHAINED || tiles == 0)) store_state(p.state_out, srow, p.state_bf16, h);
+    barrier_lds();
+    Tile cur = uniform(sh.tile[0]);
+    for (int i = 1; cur.n >= 0; ++i) {
+        const int rows = min(max(cur.len - cur.index * TILE - wave * S, 0), S);  // of this wave
+        const uint32_t off = lane_offset<T>(p, cur, lane);
+        const int64_t token = (int64_t)cur.start + cur.index * TILE + wave * S;
+        typename two::bits rx[S], rg[S];
+        {
+            const RowBuffer<T> x(p.x, token, p.xs, p.C, rows), g(p.g, token, p.gs, p.C, rows);
+#pragma unroll
+            for (int j = S - 1; j >= 0; --j) {
+                rg[j] = g.load(off, j);
+                rx[j] = x.load(off, j);
+            }
+        }
+        if (rows < S) {
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (j >= rows) {
+                    rx[j] = two::both(0.f);
+                    rg[j] = two::both(open_gate<GATE>());
+                }
+        }
+        float a[S][2], u[S][2];
+        Run<GATE> run[2];
+        auto factors = [&](int j, int v) __attribute__((always_inline)) {
+            const Factors<GATE, INPUT> f(two::get(rg[j], v));
+            a[j][v] = f.a;
+            u[j][v] = f.input(two::get(rx[j], v));
+            return f;
+        };
+#pragma unroll
+        for (int j = S - 1; j >= 0; --j) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const Factors<GATE, INPUT> f = factors(j, v);
+                run[v].before(f, u[j][v]);
+            }
+            if (j % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
+        }
+        sh.steps[wave][lane] = make_float4(run[0].log2_decay(), run[1].log2_decay(), run[0].add, run[1].add);
+        barrier_lds();
+        const Tile after = uniform(sh.tile[i & 1]);
+        barrier_lds();
+        if (AGAIN) {
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                two::hold(rg[j]);
+                two::hold(rx[j]);
+            }
+        }
+        float2 h = begin_state(sh, lane, wave);
+        const RowBuffer<T> o(p.o, token, p.os, p.C, rows);
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            if (AGAIN) {
+                factors(j, 0);
+                factors(j, 1);
+            }
+            h.x = fmaf(a[j][0], h.x, u[j][0]);
+            h.y = fmaf(a[j][1], h.y, u[j][1]);
+            o.store(off, j, h.x, h.y);
+            if (AGAIN && (j + 1) % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
+        }
+        cur = after;
+    }
 }
 
 // The gradients: r_t, what the tokens behind t leave for h_t, runs the other way,
 //     dh_t = do_t + r_t,  r_{t-1} = a_t dh_t,
-// as steps (P, H) of r -> P r + H with H = sum_t do_t exp2(l_first + .. + l_t).  The chain
-// position of a wave counts from the tile's end, that of a tile from the sequence's end.
+// as steps (P, H) of r -> P r + H with H = sum_t do_t a_first .. a_t.  The chain position
+// of a wave counts from the tile's end, that of a tile from the sequence's end.
 template <typename T, int GATE, int INPUT, bool CHAINED>
-__global__ void __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 4 : 2) scan_backward_kernel(ScanParams p) {
-    typedef typename Pair<T>::vec vec;
-    constexpr int S = sizeof(T) == 2 ? kRows : kRows / 2, TILE = S * kWaves;
+__global__ void __launch_bounds__(64 * (scan_waves(CHAINED) + 1), scan_occupancy(sizeof(T), true, scan_cheap(GATE, INPUT))) scan_backward_kernel(ScanParams p) {
+    typedef Two<T> two;
+    constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), true, CHEAP);
+    constexpr int WAVES = scan_waves(CHAINED), S = scan_rows(sizeof(T), true, GATE, INPUT), TILE = S * WAVES;
     constexpr bool X = INPUT != KDA_INPUT_PLAIN;
-    __shared__ float4 steps[2][kWaves][64];
-    __shared__ float2 carry[64];
-    __shared__ TileId shared_id;
+    __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const TileId id = CHAINED ? chained_tile<TILE>(p, wave, lane, &shared_id, true) : whole_sequence(p);
-    if (id.n < 0) return;
-    const int c = id.group * 128 + 2 * lane;
-    const bool on = c < p.C;
-    const int cl = on ? c : p.C - 2;
-    const size_t srow = (size_t)id.n * p.C + cl;
-    const int tiles = (int)((id.len + TILE - 1) / TILE);
-
-    vec rd[S], rg[S], rh[S], rx[X ? S : 1];
-    auto load = [&](int i) __attribute__((always_inline)) {
-        const int64_t t0 = (int64_t)i * TILE + wave * S;
+    auto at = [&](const Tile &t) { return (size_t)t.n * p.C + t.group * 128 + 2 * lane; };
+    auto on = [&](const Tile &t) { return t.group * 128 + 2 * lane < p.C; };
+    if (wave == WAVES) {
+        manage<TILE, true, CHAINED, WAVES>(
+            p, sh, lane,
+            [&](const Tile &t) { return p.dstate_out && on(t) ? *reinterpret_cast<const float2 *>(p.dstate_out + at(t)) : float2{0.f, 0.f}; },
+            [&](const Tile &t, float2 r) { if (p.dstate_in && on(t)) *reinterpret_cast<float2 *>(p.dstate_in + at(t)) = r; });
+        return;
+    }
+    const int pos = WAVES - 1 - wave;
+    barrier_lds();
+    Tile cur = uniform(sh.tile[0]);
+    for (int i = 1; cur.n >= 0; ++i) {
+        const int t0 = cur.index * TILE + wave * S, rows = min(max(cur.len - t0, 0), S);  // of this wave
+        const int first = t0 == 0;
+        const uint32_t off = lane_offset<T>(p, cur, lane);
+        const int64_t token = (int64_t)cur.start + t0;
+        typename two::bits rd[S], rg[S], rh[S], rx[X ? S : 1];
+        {
+            const RowBuffer<T> d(p.d, token, p.ds, p.C, rows), g(p.g, token, p.gs, p.C, rows);
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                rg[j] = g.load(off, j);
+                rd[j] = d.load(off, j);
+            }
+            const RowBuffer<T> h(p.o, token - 1 + first, p.os, p.C, rows);  // the tokens before
+            const RowBuffer<T> x(p.x, token, p.xs, p.C, X ? rows : 0);
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                rh[j] = h.load(off, j - first);
+                if (X) rx[X ? j : 0] = x.load(off, j);
+            }
+        }
+        const float2 h0 = first && p.state_in && on(cur) ? load_state(p.state_in, at(cur), p.state_bf16) : float2{0.f, 0.f};
+        if (rows < S) {
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (j >= rows) {
+                    rd[j] = two::both(0.f);
+                    rg[j] = two::both(open_gate<GATE>());
+                }
+        }
+        Factors<GATE, INPUT> f[S][2];
+        Run<GATE> run[2];
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-            const int64_t t = id.start + min(t0 + j, id.len - 1);
-            rd[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.d) + t * p.ds + cl);
-            rg[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.g) + t * p.gs + cl);
-            rh[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.o) + max(t - 1, id.start) * p.os + cl);
-            if (X) rx[j] = *reinterpret_cast<const vec *>(static_cast<const T *>(p.x) + t * p.xs + cl);
-        }
-    };
-    float2 r = {0.f, 0.f}, h0 = {0.f, 0.f};
-    const int last = CHAINED ? min(id.index, tiles - 1) : tiles - 1, end = CHAINED ? id.index : 0;
-    if (last >= end) load(last);
-    if (p.dstate_out && last == tiles - 1) r = *reinterpret_cast<const float2 *>(p.dstate_out + srow);
-    if (p.state_in && end == 0) h0 = load_state(p.state_in, srow, p.state_bf16);
-    for (int i = last; i >= end; --i) {
-        const int64_t t0 = (int64_t)i * TILE + wave * S;
-        float sum[2] = {0.f, 0.f}, add[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < S; ++j)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                const bool in = t0 + j < id.len;
-                const Factors<GATE, INPUT> f(to_f32(rg[j][v]));
-                sum[v] += in ? f.l : 0.f;
-                add[v] = fmaf(in ? to_f32(rd[j][v]) : 0.f, exp2_fast(sum[v]), add[v]);
+                f[j][v] = Factors<GATE, INPUT>(two::get(rg[j], v));
+                run[v].behind(f[j][v], two::get(rd[j], v));
             }
-        const int pos = kWaves - 1 - wave;
-        float4(*st)[64] = steps[CHAINED ? 0 : i & 1];
-        st[pos][lane] = make_float4(sum[0], sum[1], add[0], add[1]);
-        __syncthreads();
-        float2 mine = {0.f, 0.f};
-        if (CHAINED) {
-            if (wave == 0) {
-                const float2 before = chain_carry<kWaves>(p, id, lane, tiles - 1, tiles, st, r);
-                carry[lane] = before;
-                float2 after = before;
-                if (i == 0 && p.dstate_in) {
-                    join<kWaves>(st, lane, 0, after, mine);
-                    if (on) *reinterpret_cast<float2 *>(p.dstate_in + srow) = after;
-                }
-            }
-            __syncthreads();
-            r = carry[lane];
+            if ((j + 1) % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
-        join<kWaves>(st, lane, pos, r, mine);
-        T *dx = static_cast<T *>(p.dx) + (id.start + t0) * p.dxs + cl;
-        T *dg = static_cast<T *>(p.dg) + (id.start + t0) * p.dgs + cl;
+        sh.steps[pos][lane] = make_float4(run[0].log2_decay(), run[1].log2_decay(), run[0].add, run[1].add);
+        barrier_lds();
+        const Tile after = uniform(sh.tile[i & 1]);
+        barrier_lds();
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            two::hold(rd[j]);
+            two::hold(rh[j]);
+            if (X) two::hold(rx[X ? j : 0]);
+            if (AGAIN) two::hold(rg[j]);
+        }
+        float2 r = begin_state(sh, lane, pos);
+        const RowBuffer<T> dx(p.dx, token, p.dxs, p.C, rows), dg(p.dg, token, p.dgs, p.C, rows);
 #pragma unroll
         for (int j = S - 1; j >= 0; --j) {
-            const bool in = t0 + j < id.len;
-            float m[2] = {mine.x, mine.y}, ox[2], og[2];
+            float m[2] = {r.x, r.y}, ox[2], og[2];
             const float hs[2] = {h0.x, h0.y};
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                const Factors<GATE, INPUT> f(to_f32(rg[j][v]));
-                const float dh = to_f32(rd[j][v]) + m[v], a = exp2_fast(f.l);
-                const float before = t0 + j == 0 ? hs[v] : to_f32(rh[j][v]);
-                f.gradient(a, dh, before, X ? to_f32(rx[X ? j : 0][v]) : 0.f, ox[v], og[v]);
-                if (in) m[v] = a * dh;
+                if (AGAIN) f[j][v] = Factors<GATE, INPUT>(two::get(rg[j], v));
+                const float dh = two::get(rd[j], v) + m[v];
+                const float before = j == 0 && first ? hs[v] : two::get(rh[j], v);
+                f[j][v].gradient(dh, before, X ? two::get(rx[X ? j : 0], v) : 0.f, ox[v], og[v]);
+                m[v] = f[j][v].a * dh;  // (a row that only pads has an open gate and no gradient of its own)
             }
-            mine = make_float2(m[0], m[1]);
-            if (in && on) {
-                Pair<T>::store(dx + j * p.dxs, ox[0], ox[1]);
-                Pair<T>::store(dg + j * p.dgs, og[0], og[1]);
-            }
+            r = make_float2(m[0], m[1]);
+            dx.store(off, j, ox[0], ox[1]);
+            dg.store(off, j, og[0], og[1]);
+            if (AGAIN && j % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
-        if (!CHAINED && i > end) load(i - 1);
+        cur = after;
     }
-    if (p.dstate_in && on && wave == 0 && (!CHAINED || tiles == 0))
-        *reinterpret_cast<float2 *>(p.dstate_in + srow) = r;
 }
 
-// Marks every word of the workspace as not yet written and sets the ticket to 0.
-__global__ void __launch_bounds__(256) scan_clear_kernel(uint4 *words, int64_t count, uint32_t *ticket) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256)
-        words[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+// Workspace of the chained schedule: the ticket, the flags [groups][tiles] and the words
+// [tiles][groups][128].
+struct ChainLayout {
+    int64_t flags, words, bytes;  // byte offsets, all of 256
+    ChainLayout(int64_t tiles, int64_t groups) {
+        flags = 256;
+        words = flags + (groups * tiles * 4 + 255) / 256 * 256;
+        bytes = words + tiles * groups * 128 * 8;
+    }
+};
+
+// Marks every word as not yet written, and sets flags and ticket to 0.
+__global__ void __launch_bounds__(256) scan_clear_kernel(uint4 *ws, int64_t words, int64_t end) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < end; i += (int64_t)gridDim.x * 256) {
+        const uint32_t v = i < words ? 0u : kEmpty;
+        ws[i] = make_uint4(v, v, v, v);
+    }
 }
 
 template <typename T, int GATE, int INPUT> void launch(const ScanParams &p, bool chained, bool backward, unsigned blocks, hipStream_t s) {
-    const dim3 grid(blocks), block(64 * kWaves);
+    const dim3 grid(blocks), block(64 * (scan_waves(chained) + 1));
     if (backward) {
         if (chained) hipLaunchKernelGGL((scan_backward_kernel<T, GATE, INPUT, true>), grid, block, 0, s, p);
         else hipLaunchKernelGGL((scan_backward_kernel<T, GATE, INPUT, false>), grid, block, 0, s, p);
@@ -243,14 +329,16 @@ template <typename T, int GATE> void launch(const ScanParams &p, int input, bool
 hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate, int input, bool backward, hipStream_t s) {
     unsigned blocks = (unsigned)((int64_t)p.N * p.groups);
     if (plan.chained) {
-        p.tiles = plan.tiles;
-        p.ticket = static_cast<uint32_t *>(plan.workspace);
-        p.words = reinterpret_cast<uint64_t *>(static_cast<char *>(plan.workspace) + 256);
+        p.tiles = (int)plan.tiles;
+        char *ws = static_cast<char *>(plan.workspace);
+        const ChainLayout at(plan.tiles, p.groups);
+        p.ticket = reinterpret_cast<uint32_t *>(ws);
+        p.flags = reinterpret_cast<uint32_t *>(ws + at.flags);
+        p.words = reinterpret_cast<uint64_t *>(ws + at.words);
         p.polls = spin_limit();
         blocks = (unsigned)(plan.tiles * p.groups);
-        const int64_t count = plan.tiles * p.groups * 64;
-        const unsigned cb = (unsigned)std::min<int64_t>((count + 255) / 256, 4096);
-        hipLaunchKernelGGL(scan_clear_kernel, dim3(cb), dim3(256), 0, s, reinterpret_cast<uint4 *>(p.words), count, p.ticket);
+        const unsigned cb = (unsigned)std::min<int64_t>((at.bytes / 16 + 255) / 256, 2048);
+        hipLaunchKernelGGL(scan_clear_kernel, dim3(cb), dim3(256), 0, s, reinterpret_cast<uint4 *>(ws), at.words / 16, at.bytes / 16);
         trace("scan_clear_kernel grid=(%u) block=256", cb);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -259,13 +347,17 @@ hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate
                                              : launch<__bf16, KDA_GATE_SIGMOID>(p, input, plan.chained, backward, blocks, s);
     else gate == KDA_GATE_LOG ? launch<float, KDA_GATE_LOG>(p, input, plan.chained, backward, blocks, s)
                               : launch<float, KDA_GATE_SIGMOID>(p, input, plan.chained, backward, blocks, s);
-    trace("scan%s_kernel<%s> grid=(%u) block=%d", backward ? "_backward" : "", plan.chained ? "chained" : "one pass", blocks, 64 * kWaves);
+    trace("scan%s_kernel<%s> grid=(%u) block=%d", backward ? "_backward" : "", plan.chained ? "chained" : "one pass", blocks, 64 * (scan_waves(plan.chained) + 1));
     return hipGetLastError();
 }
 
 }  // namespace
 
-int scan_tile(kda_dtype dt, bool backward) { return kWaves * (backward && dt == KDA_F32 ? kRows / 2 : kRows); }
+int scan_tile(kda_dtype dt, int gate, int input, bool backward, bool chained) {
+    return scan_waves(chained) * scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
+}
+
+size_t scan_chain_bytes(int64_t tiles, int C) { return (size_t)ChainLayout(tiles, ((int64_t)C + 127) / 128).bytes; }
 
 hipError_t launch_gated_scan(const kda_gated_scan_args *a, const ScanPlan &plan, hipStream_t s) {
     ScanParams p = {};

@@ -14,7 +14,7 @@ namespace {
 
 using namespace kda::checks;
 
-// A launch holds fewer than 2^32 threads, 512 of them in a workgroup.
+// A launch holds fewer than 2^32 threads, up to 1024 of them in a workgroup.
 constexpr int64_t kMaxGroups = (int64_t)1 << 22;
 
 int64_t channel_groups(int32_t C) { return ((int64_t)C + 127) / 128; }
@@ -29,6 +29,15 @@ kda_status check_scan(int32_t N, int32_t C, kda_dtype dt, int gate, int input, u
         return fail(KDA_ERR_INVALID_ARG, "input_kind %d: use a KDA_INPUT_* value", input);
     if (flags & ~(uint32_t)KDA_F_STATE_BF16) return fail(KDA_ERR_UNSUPPORTED, "unsupported flags 0x%x", flags);
     if (N * channel_groups(C) >= kMaxGroups) return fail(KDA_ERR_INVALID_ARG, "num_seqs * channels too large");
+    return KDA_OK;
+}
+
+// Tokens a wave's buffer spans at once, times this many elements, stay below 2^31 bytes.
+constexpr int64_t kMaxStride = (int64_t)1 << 22;
+kda_status check_strides(const Rows *r, int n) {
+    for (int i = 0; i < n; ++i)
+        if (r[i].stride > kMaxStride)
+            return fail(KDA_ERR_UNSUPPORTED, "%s_stride = %lld, at most %lld", r[i].name, (long long)r[i].stride, (long long)kMaxStride);
     return KDA_OK;
 }
 
@@ -56,19 +65,49 @@ template <typename A> int64_t longest_sequence(const A &a) {
     return longest;
 }
 
+// Tokens that the tiles of a chained call hold, the half-empty last ones among them.
+template <typename A> double padded_tokens(const A &a, int tile) {
+    const int64_t T = a.total_tokens, N = a.num_seqs;
+    if (a.cu_seqlens && !a.cu_seqlens_host) return (double)T + 0.5 * tile * (double)N;
+    int64_t tiles = 0;
+    for (int64_t n = 0; n < N; ++n) {
+        const int64_t len = a.cu_seqlens ? (int64_t)a.cu_seqlens_host[n + 1] - a.cu_seqlens_host[n] : T / N;
+        tiles += (len + tile - 1) / tile;
+    }
+    return (double)tiles * tile;
+}
+
+// The automatic choice compares a cost of both sides (us).  One pass takes the longer of
+// its longest sequence, token behind token, and of the memory's time for everything, at
+// 4.8 TB/s.  Chained takes 8 for its second launch and its workspace, and the memory's
+// time at 4.7 to 5.2 TB/s, of which a row that only pads a last tile costs half.  Measured,
+// one pass / chained, 4096 channels of bf16: 1 sequence of 224 tokens 10.5/14.0, 448
+// 16.6/14.5, 4096 137/35; 8 of 1000 47/52; 64 of 1000, log-decays 326/309, pre-activations
+// with complement 320/375; backward, 8 of 2000 142/137.  Lengths that only the device
+// knows count as one sequence: chained loses up to a third on many short ones, one pass
+// any factor on a long one among them.
+template <typename A> bool prefer_chained(const A &a, bool backward, int tile) {
+    const bool half = a.dtype == KDA_BF16, cheap = a.gate_kind == KDA_GATE_LOG && a.input_kind == KDA_INPUT_PLAIN;
+    const double row = (double)a.channels * (half ? 2 : 4) * (!backward ? 3 : a.input_kind == KDA_INPUT_PLAIN ? 5 : 6);
+    const double token = backward ? (half ? 0.051 : 0.072) : (half ? 0.031 : 0.042);
+    const double rate = backward ? 5.0e6 : cheap ? 5.2e6 : 4.7e6;
+    const double T = (double)a.total_tokens;
+    const double one = std::max((double)longest_sequence(a) * token, T * row / 4.8e6);
+    return 8.0 + 0.5 * (T + padded_tokens(a, tile)) * row / rate < one;
+}
+
 // The schedule of a call that has a workspace.
 template <typename A> kda::ScanPlan scan_plan(const A &a, bool backward) {
     const kda::ScanPlan one{false, 0, nullptr};
     if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.total_tokens < 1) return one;
-    const int tile = kda::scan_tile(a.dtype, backward);
+    const int tile = kda::scan_tile(a.dtype, a.gate_kind, a.input_kind, backward, true);
     const kda::ScanPlan chained{true, a.total_tokens / tile + a.num_seqs, a.workspace};
     if (chained.tiles * channel_groups(a.channels) >= kMaxGroups) return one;
-    if (a.schedule == KDA_SCHEDULE_CHAINED) return chained;
-    return longest_sequence(a) > tile ? chained : one;
+    return a.schedule == KDA_SCHEDULE_CHAINED || prefer_chained(a, backward, tile) ? chained : one;
 }
 
 size_t plan_bytes(const kda::ScanPlan &plan, int32_t C) {
-    return plan.chained ? 256 + (size_t)(plan.tiles * channel_groups(C)) * 128 * 8 : 0;
+    return plan.chained ? kda::scan_chain_bytes(plan.tiles, C) : 0;
 }
 
 template <typename A> size_t scan_workspace(const A *a, bool backward) {
@@ -125,6 +164,8 @@ kda_status scan_prefill_impl(kda_gated_scan_args a, hipStream_t stream) {
         st = check_rows(x);
         if (st != KDA_OK) return st;
     }
+    st = check_strides(r, 3);
+    if (st != KDA_OK) return st;
     a.o_stride = r[0].stride; a.x_stride = r[1].stride; a.gate_stride = r[2].stride;
     if ((uintptr_t)a.state_in % 16 || (uintptr_t)a.state_out % 16)
         return fail(KDA_ERR_INVALID_ARG, "the states must be 16-byte aligned");
@@ -189,6 +230,8 @@ kda_status scan_backward_impl(kda_gated_scan_backward_args a, hipStream_t stream
         st = check_rows(x);
         if (st != KDA_OK) return st;
     }
+    st = check_strides(r, 6);
+    if (st != KDA_OK) return st;
     a.dx_stride = r[0].stride; a.dgate_stride = r[1].stride; a.d_o_stride = r[2].stride;
     a.gate_stride = r[3].stride; a.o_stride = r[4].stride; a.x_stride = r[5].stride;
     if ((uintptr_t)a.state_in % 16 || (uintptr_t)a.dstate_out % 16 || (uintptr_t)a.dstate_in % 16)

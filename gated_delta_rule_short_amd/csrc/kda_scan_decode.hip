@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepParams p) {
             const Factors<GATE, INPUT> f(z[i]);
             const float u = f.input(x[i]), limited = __builtin_amdgcn_fmed3f(h[i], -3.4028234663852886e38f, 3.4028234663852886e38f);
             // (an infinite state stays one: infinity minus a part of itself would not)
-            h[i] = f.c < 0.5f ? h[i] + fmaf(-f.c, limited, u) : fmaf(exp2_fast(f.l), h[i], u);
+            h[i] = f.c < 0.5f ? h[i] + fmaf(-f.c, limited, u) : fmaf(f.a, h[i], u);
         }
         store4(state, h);
         store4(static_cast<T *>(p.o) + n * p.os + c, h);

@@ -694,20 +694,22 @@ typedef struct {
 } kda_gated_scan_args;
 
 /* Packed prompts, every sequence from its initial state to its final one; empty
- * sequences pass their state through.  Two schedules (same results, bit for bit):
+ * sequences pass their state through.  Two schedules (results agree to rounding, and
+ * each is the same from run to run):
  *   - one pass: a workgroup walks a sequence, 128 channels wide; no workspace;
  *   - chained: workgroups take tiles of a sequence side by side and hand the state from
  *     tile to tile through the workspace, after a launch that clears it.  A tile waits
  *     only for tiles that run or have run, so every wait ends; kda_set_spin_limit bounds
  *     it all the same, and a wait that gives up makes its outputs NaN.
- * KDA_SCHEDULE_AUTO takes the faster one where a workspace is given, by the longest
- * sequence that cu_seqlens_host (or equal sequences) shows, else by T.  The workspace is
- * overwritten by each call and must not be shared by calls that may overlap in time. */
+ * KDA_SCHEDULE_AUTO takes the one expected to be faster where a workspace is given, by the
+ * lengths that cu_seqlens_host (or equal sequences) shows; without them it takes the
+ * batch for one long sequence.  The workspace is overwritten by each call and must not be
+ * shared by calls that may overlap in time.  A token stride is at most 2^22 elements. */
 kda_status kda_gated_scan_prefill(const kda_gated_scan_args *args, hipStream_t stream);
 
 /* Workspace bytes of the schedule that a call runs when it is given one (0: one pass).
- * Depends on num_seqs, channels, total_tokens, dtype, schedule, cu_seqlens_host and
- * whether cu_seqlens is given. */
+ * Depends on num_seqs, channels, total_tokens, dtype, gate_kind, input_kind, schedule,
+ * cu_seqlens_host and whether cu_seqlens is given. */
 size_t kda_gated_scan_workspace_size(const kda_gated_scan_args *args);
 
 typedef struct {

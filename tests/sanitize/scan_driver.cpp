@@ -20,7 +20,8 @@ static kda::ScanPlan g_plan;
 static char g_msg[512];
 
 namespace kda {
-int scan_tile(kda_dtype dt, bool backward) { return backward && dt == KDA_F32 ? 64 : 128; }
+int scan_tile(kda_dtype dt, int, int, bool backward, bool chained) { return (chained ? 30 : 14) * (dt == KDA_F32 ? 1 : 2) * (backward ? 2 : 4); }
+size_t scan_chain_bytes(int64_t tiles, int C) { return 256 + (size_t)((C + 127) / 128) * tiles * 1024; }
 hipError_t launch_gated_scan(const kda_gated_scan_args *a, const ScanPlan &p, hipStream_t) {
     ++g_launch; g_scan = *a; g_plan = p; return hipSuccess;
 }
@@ -60,9 +61,9 @@ int main() {
     CHECK(kda_gated_scan_prefill(&s, nullptr) == KDA_OK && g_launch == 1 && !g_plan.chained);
     CHECK(g_scan.x_stride == 408 && g_scan.o_stride == 200);
     const size_t need = kda_gated_scan_workspace_size(&s);
-    CHECK(need == 256 + (size_t)(1000 / 128 + 2) * 2 * 128 * 8);
+    CHECK(need == 256 + 2 * (size_t)(1000 / 240 + 2) * 1024);
     s.workspace = addr(5); s.workspace_bytes = need;
-    CHECK(kda_gated_scan_prefill(&s, nullptr) == KDA_OK && g_plan.chained && g_plan.tiles == 9 && g_plan.workspace == addr(5));
+    CHECK(kda_gated_scan_prefill(&s, nullptr) == KDA_OK && g_plan.chained && g_plan.tiles == 6 && g_plan.workspace == addr(5));
     s.workspace_bytes = need - 1;
     CHECK(kda_gated_scan_prefill(&s, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 2);
     s.schedule = KDA_SCHEDULE_ONE_PASS;
@@ -85,7 +86,7 @@ int main() {
     b.dstate_out = static_cast<const float *>(addr(6)); b.dstate_in = static_cast<float *>(addr(6));
     b.cu_seqlens = iaddr(7); b.workspace = addr(8);
     b.workspace_bytes = kda_gated_scan_backward_workspace_size(&b);
-    CHECK(b.workspace_bytes == 256 + (size_t)(1000 / 64 + 2) * 128 * 8);
+    CHECK(b.workspace_bytes == 256 + (size_t)(1000 / 60 + 2) * 1024);
     CHECK(kda_gated_scan_backward(&b, nullptr) == KDA_OK && g_plan.chained && g_grad.dgate_stride == 128 && g_launch == 5);
     b.x = nullptr;
     CHECK(kda_gated_scan_backward(&b, nullptr) == KDA_ERR_INVALID_ARG && g_launch == 5);

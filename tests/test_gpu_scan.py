@@ -8,7 +8,8 @@ from tests._scan_common import (BF, DEV, F32, KINDS, U32, backward_ref, check, c
                                 make_scan, scan_ref)
 
 pytestmark = pytest.mark.gpu
-SHAPES = [([1], 8), ([0, 1, 2], 120), ([15, 16, 17, 0], 128), ([127, 128, 129, 1], 136), ([300, 0, 700, 64], 264)]
+SHAPES = [([1], 8), ([0, 1, 2], 120), ([15, 16, 17, 0], 128), ([127, 128, 129, 1], 136), ([300, 0, 700, 64], 264),
+          ([239, 240, 241, 480], 72)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -124,6 +125,23 @@ def test_rows_behind_the_last_sequence_stay(schedule):
     assert (dx[290:] == 5.0).all() and (dg[290:] == 6.0).all()
 
 
+@pytest.mark.parametrize("count", [63, 64, 65, 4100])
+@pytest.mark.parametrize("schedule", ["one_pass", "chained"])
+def test_many_sequences(count, schedule):
+    """More sequences than a wave has lanes, and than two steps of its search tell apart."""
+    gen = torch.Generator().manual_seed(count)
+    lengths = torch.randint(0, 4, (count,), generator=gen).tolist()
+    lengths[count // 2] = 500
+    inp = make_scan(lengths, 16, F32, "log", pool=count + 3, seed=count, device=DEV)
+    before = inp["state"].clone()
+    o, pool = kda.kda_gated_scan_prefill(inp["x"], inp["gate"], cu_seqlens=inp["cu"], state_in=inp["state"],
+                                         state_out=inp["state"], state_slots=inp["slots"], schedule=schedule)
+    check_scan(o, pool[inp["slots"].long()], dict(inp, state=before), "log", "plain")
+    dense = dict(inp, state=before[inp["slots"].long()].contiguous(), slots=None)
+    d_o, o, ds, got = _grads(dense, "log", "plain", F32, schedule=schedule)
+    check_backward(got, dense, d_o, o, ds, "log", "plain")
+
+
 def test_many_tiles_and_repeatability():
     """A long chain beside short ones: bitwise the same from run to run, and the sequences
     of a ragged batch as on their own."""
@@ -156,9 +174,9 @@ def test_long_memories_keep_their_length(schedule):
     z = g[0, 0].double().cpu()
     want = -torch.expm1(z * torch.arange(1, T + 1, dtype=torch.float64)) / -torch.expm1(z)
     at = torch.tensor([0, 100, 5000, 30000, 59999])
-    # one rounding of the exponential for each wave's 16 tokens and each tile of 128, of both
-    # u32 at most, over the 10,000 tokens that count: 79 + 2 tiles' steps beside the sums
-    bound = 3 * (10000 / 128 + 32) * U32 * want[at][:, None]
+    # one rounding of the exponential (1 ulp = 2 u32) and of the step (u32) for each tile, of
+    # 56 tokens or more, over the 10,000 tokens that count, and those of a tile's sums
+    bound = 3 * (10000 / 56 + 32) * U32 * want[at][:, None]
     check(o[at], want[at][:, None].expand(-1, C), bound.expand(-1, C), "o")
     check(state, want[-1].expand(1, C), float(bound[-1]), "state")
     h = torch.zeros(1, C, device=DEV)
@@ -298,7 +316,7 @@ def test_a_wait_that_gives_up_ends_the_call():
         kda.set_spin_limit(0)
     assert old > 1
     ok = ~torch.isnan(got)
-    assert torch.equal(got[ok], want[ok]) and ok[:128].all()
+    assert torch.equal(got[ok], want[ok]) and ok[:56].all()
     got, _ = _prefill(inp, "log", "plain", schedule="chained")
     assert torch.equal(got, want)
 
@@ -361,8 +379,6 @@ def test_two_streams_at_once():
 def test_automatic_schedule_and_no_workspace():
     inp = make_scan([300, 5], 136, F32, "log", seed=16, device=DEV)
     whole = _prefill(inp, "log", "plain", schedule="one_pass")
-    chained = _prefill(inp, "log", "plain", schedule="chained")
-    assert all(torch.equal(p, q) for p, q in zip(whole, chained))
     for kw in ({"workspace": None}, {"workspace": False}, {"workspace": None, "cu_seqlens_host": inp["cu_host"]}):
         got = _prefill(inp, "log", "plain", **kw)
         assert all(torch.equal(p, q) for p, q in zip(whole, got))
