@@ -1,8 +1,8 @@
 // kda_add_norm.hip -- residual addition, RMS norm of whole rows and 8-bit output with
 // scales, and the gradients of the norm.
 //
-// A row of C channels lies in the registers of WPR waves, NC runs of eight channels a
-// lane, from its read to its last write: every element is read once and written once and
+// A row of C channels lies in the registers of WPR waves, one or two runs of eight channels
+// a lane, from its read to its last write: every element is read once and written once and
 // the bound is HBM.
 #include <algorithm>
 
@@ -24,6 +24,21 @@ template <> __device__ __forceinline__ void load8<float>(const float *p, float (
 #pragma unroll
     for (int i = 0; i < 4; ++i) { x[i] = a[i]; x[4 + i] = b[i]; }
 }
+// Eight elements as they were read.
+template <typename T> struct Eight;
+template <> struct Eight<__bf16> {
+    bf16x8 v;
+    __device__ __forceinline__ void load(const __bf16 *p) { v = *reinterpret_cast<const bf16x8 *>(p); }
+    __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+};
+template <> struct Eight<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = reinterpret_cast<const f32x4 *>(p)[0];
+        b = reinterpret_cast<const f32x4 *>(p)[1];
+    }
+    __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
 __device__ __forceinline__ void store8(__bf16 *p, const float (&x)[8]) {
     *reinterpret_cast<bf16x8 *>(p) = pack8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
 }
@@ -114,7 +129,7 @@ __global__ void __launch_bounds__(64 * WPR) add_norm_kernel(NormParams p) {
         ss = wave_sum(ss);
         if (WPR > 1) {
             if (lane == 0) part[buf][wave] = ss;
-            __syncthreads();
+            barrier_lds();
             ss = 0.f;
 #pragma unroll
             for (int q = 0; q < WPR; ++q) ss += part[buf][q];
@@ -150,7 +165,7 @@ __global__ void __launch_bounds__(64 * WPR) add_norm_kernel(NormParams p) {
             top = wave_max(top);
             if (WPR > 1) {
                 if (lane == 0) tops[buf][wave] = top;
-                __syncthreads();
+                barrier_lds();
 #pragma unroll
                 for (int q = 0; q < WPR; ++q) top = max(top, tops[buf][q]);
             }
@@ -176,113 +191,160 @@ struct GradParams {
     float eps;
 };
 
-// A workgroup takes rows blockIdx, blockIdx + gridDim, .. and keeps the sums of dy n of its
-// own channels in registers.
-template <typename T, int WPR, int NC>
-__global__ void __launch_bounds__(64 * WPR) add_norm_backward_kernel(GradParams p) {
-    __shared__ float2 part[2][WPR];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    float dw[NC][8] = {};
+__device__ __forceinline__ void weights(const float *p, int at, float (&w)[8]) {
+    if (p) {
+        load8<float>(p + at, w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    }
+}
+
+// A workgroup of ROWS x WPR waves takes rows blockIdx x ROWS and on, a grid's rows apart,
+// with the next ones on their way while it works on these, and keeps the sums of dy n of
+// its channels in registers; its waves' sums meet in LDS at the end, one after another.
+template <typename T, int WPR, int NC, int ROWS>
+__global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(GradParams p) {
+    __shared__ float2 part[2][ROWS][WPR];
+    __shared__ float meet[ROWS > 1 ? ROWS - 1 : 1][ROWS > 1 ? 512 * WPR * NC : 1];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64 % WPR, sub = threadIdx.x / (64 * WPR);
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    // (sixteen waves leave a lane 128 registers: there the weights are read again, and the
+    // residual's gradient when it is needed)
+    constexpr bool KEEP = WPR < 16;
+    float dw[NC][8] = {}, w[KEEP ? NC : 1][8];
+    Eight<T> ns[NC], ng[NC], nr[NC];
+    bool on[NC];
+    int at[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = 8 * (lane + 64 * (wave + WPR * i));
+        on[i] = c < p.C;
+        at[i] = on[i] ? c : 0;
+        if (KEEP) weights(p.w, at[i], w[KEEP ? i : 0]);
+    }
+    auto load = [&](int64_t t) __attribute__((always_inline)) {
+        t = min(t, p.T - 1);  // (rows past the last one read it again and leave nothing)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            ns[i].load(static_cast<const T *>(p.s) + t * p.ss + at[i]);
+            ng[i].load(static_cast<const T *>(p.dy) + t * p.dys + at[i]);
+            if (KEEP && p.dr) nr[i].load(static_cast<const T *>(p.dr) + t * p.drs + at[i]);
+        }
+    };
+    int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+    load(t);
+    // every wave of a workgroup makes the same turns: barriers stand inside
     int buf = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
-        float s[NC][8], g[NC][8];
+    for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < p.T; t0 += step, t += step, buf ^= 1) {
+        Eight<T> s[NC], g[NC], r[NC];
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = 8 * (lane + 64 * (wave + WPR * i));
-            if (c < p.C) {
-                load8<T>(static_cast<const T *>(p.s) + t * p.ss + c, s[i]);
-                load8<T>(static_cast<const T *>(p.dy) + t * p.dys + c, g[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[i][j] = g[i][j] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = 8 * (lane + 64 * (wave + WPR * i));
-            float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-            if (p.w && c < p.C) load8<float>(p.w + c, w);
+            s[i] = ns[i];
+            g[i] = ng[i];
+            if (KEEP) r[i] = nr[i];
+            float a = 0.f, b = 0.f;
+            if (!KEEP) weights(p.w, at[i], w[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fmaf(s[i][j], s[i][j], ss);
-                dot = fmaf(s[i][j], g[i][j] * w[j], dot);
+                const float x = s[i].get(j);
+                a = fmaf(x, x, a);
+                b = fmaf(x, g[i].get(j) * w[KEEP ? i : 0][j], b);
             }
+            ss += on[i] ? a : 0.f;
+            dot += on[i] ? b : 0.f;
         }
+        load(t + step);
         ss = wave_sum(ss);
         dot = wave_sum(dot);
         if (WPR > 1) {
-            if (lane == 0) part[buf][wave] = make_float2(ss, dot);
-            __syncthreads();
+            if (lane == 0) part[buf][sub][wave] = make_float2(ss, dot);
+            barrier_lds();
             ss = dot = 0.f;
 #pragma unroll
-            for (int q = 0; q < WPR; ++q) { ss += part[buf][q].x; dot += part[buf][q].y; }
+            for (int q = 0; q < WPR; ++q) { ss += part[buf][sub][q].x; dot += part[buf][sub][q].y; }
         }
         const float rs = rsqrtf(ss / (float)p.C + p.eps), k = dot / (float)p.C * rs * rs;
+        if (t < p.T) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = 8 * (lane + 64 * (wave + WPR * i));
-            if (c >= p.C) continue;
-            float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, d[8];
-            if (p.w) load8<float>(p.w + c, w);
+            for (int i = 0; i < NC; ++i) {
+                float d[8];
+                if (!KEEP) {
+                    weights(p.w, at[i], w[0]);
+                    if (p.dr) r[i].load(static_cast<const T *>(p.dr) + t * p.drs + at[i]);
+                }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(g[i][j], s[i][j] * rs, dw[i][j]);
-                d[j] = rs * (g[i][j] * w[j] - k * s[i][j]);
+                for (int j = 0; j < 8; ++j) {
+                    const float x = s[i].get(j), y = g[i].get(j);
+                    dw[i][j] = fmaf(y, x * rs, dw[i][j]);
+                    d[j] = rs * (y * w[KEEP ? i : 0][j] - k * x);
+                    if (p.dr) d[j] += r[i].get(j);
+                }
+                if (on[i]) store8(static_cast<T *>(p.dx) + t * p.dxs + at[i], d);
             }
-            if (p.dr) {
-                float r[8];
-                load8<T>(static_cast<const T *>(p.dr) + t * p.drs + c, r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] += r[j];
-            }
-            store8(static_cast<T *>(p.dx) + t * p.dxs + c, d);
         }
     }
     if (p.part) {
+        if (ROWS > 1 && sub > 0) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = 8 * (lane + 64 * (wave + WPR * i));
-            if (c < p.C) store8(p.part + (size_t)blockIdx.x * p.C + c, dw[i]);
+            for (int i = 0; i < NC; ++i) store8(&meet[sub - 1][8 * (lane + 64 * (wave + WPR * i))], dw[i]);
+        }
+        if (ROWS > 1) __syncthreads();
+        if (sub == 0) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                for (int q = 0; q < ROWS - 1; ++q) {
+                    float o[8];
+                    load8<float>(&meet[q][8 * (lane + 64 * (wave + WPR * i))], o);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dw[i][j] += o[j];
+                }
+                if (on[i]) store8(p.part + (size_t)blockIdx.x * p.C + at[i], dw[i]);
+            }
         }
     }
 }
 
-// dweight: 32 channels a workgroup, 8 lanes of four, 32 slices of the partial rows joined
+// dweight: 32 channels a workgroup, 8 lanes of four, 128 slices of the partial rows joined
 // through LDS in order.
-__global__ void __launch_bounds__(256) weight_grad_kernel(const float *part, int rows, int C, float *dw) {
-    __shared__ f32x4 sums[32][8];
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float *part, int rows, int C, float *dw) {
+    __shared__ f32x4 sums[128][8];
     const int lane = threadIdx.x % 8, slice = threadIdx.x / 8, c = blockIdx.x * 32 + 4 * lane;
     f32x4 a = {0.f, 0.f, 0.f, 0.f};
-    if (c < C) {
-        const int per = (rows + 31) / 32, end = min(rows, (slice + 1) * per);
-        for (int r = slice * per; r < end; ++r) a = a + *reinterpret_cast<const f32x4 *>(part + (size_t)r * C + c);
-    }
+    if (c < C)
+        for (int r = slice; r < rows; r += 128) a = a + *reinterpret_cast<const f32x4 *>(part + (size_t)r * C + c);
     sums[slice][lane] = a;
     __syncthreads();
-    if (slice == 0 && c < C) {
-        for (int q = 1; q < 32; ++q) a = a + sums[q][lane];
-        *reinterpret_cast<f32x4 *>(dw + c) = a;
+#pragma unroll
+    for (int half = 64; half > 0; half /= 2) {
+        if (slice < half) sums[slice][lane] = sums[slice][lane] + sums[slice + half][lane];
+        __syncthreads();
     }
+    if (slice == 0 && c < C) *reinterpret_cast<f32x4 *>(dw + c) = sums[0][lane];
 }
 
-// Waves a row takes: one where its channels fit one wave's registers (eight runs of 512)
-// and there are rows enough to fill the GPU with such waves, else four.
-constexpr int64_t kManyRows = 2048;
+// Waves a row takes: so many that a lane holds at most two runs of eight channels.  16,384
+// rows of 4096 in bf16 with 8-bit groups: 87 us with four waves of two runs, 142 with one
+// of eight; 32,768 rows of 1024 42 with one wave of two runs, 48 with four of half a run.
+int waves_of(int C) { return C <= 1024 ? 1 : C <= 2048 ? 2 : C <= 4096 ? 4 : C <= 8192 ? 8 : 16; }
 constexpr unsigned kMaxBlocks = 1u << 20;
 
 template <typename T, int QUANT, int WPR> void launch_norm(const NormParams &p, hipStream_t s) {
     const unsigned blocks = (unsigned)std::min<int64_t>(p.T, kMaxBlocks);
-    const int runs = (p.C + 512 * WPR - 1) / (512 * WPR);
     const dim3 grid(blocks), block(64 * WPR);
-    if (runs <= 1) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 1>), grid, block, 0, s, p);
-    else if (runs <= 2) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 2>), grid, block, 0, s, p);
-    else if (runs <= 4) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 4>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 8>), grid, block, 0, s, p);
-    trace("add_norm_kernel<waves=%d, runs=%d> grid=(%u) block=%d", WPR, runs, blocks, 64 * WPR);
+    if (p.C <= 512 * WPR) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 2>), grid, block, 0, s, p);
+    trace("add_norm_kernel<waves=%d> grid=(%u) block=%d", WPR, blocks, 64 * WPR);
 }
 template <typename T, int QUANT> void launch_norm(const NormParams &p, hipStream_t s) {
-    p.C <= 4096 && p.T >= kManyRows ? launch_norm<T, QUANT, 1>(p, s) : launch_norm<T, QUANT, 4>(p, s);
+    switch (waves_of(p.C)) {
+    case 1: return launch_norm<T, QUANT, 1>(p, s);
+    case 2: return launch_norm<T, QUANT, 2>(p, s);
+    case 4: return launch_norm<T, QUANT, 4>(p, s);
+    case 8: return launch_norm<T, QUANT, 8>(p, s);
+    default: return launch_norm<T, QUANT, 16>(p, s);
+    }
 }
 template <typename T> void launch_norm(const NormParams &p, int quant, hipStream_t s) {
     if (quant == KDA_QUANT_NONE) launch_norm<T, KDA_QUANT_NONE>(p, s);
@@ -290,20 +352,37 @@ template <typename T> void launch_norm(const NormParams &p, int quant, hipStream
     else launch_norm<T, KDA_QUANT_GROUP>(p, s);
 }
 
-template <typename T> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {
-    const int runs = (p.C + 2047) / 2048;
-    const dim3 grid(blocks), block(256);
-    if (runs <= 1) hipLaunchKernelGGL((add_norm_backward_kernel<T, 4, 1>), grid, block, 0, s, p);
-    else if (runs <= 2) hipLaunchKernelGGL((add_norm_backward_kernel<T, 4, 2>), grid, block, 0, s, p);
-    else if (runs <= 4) hipLaunchKernelGGL((add_norm_backward_kernel<T, 4, 4>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((add_norm_backward_kernel<T, 4, 8>), grid, block, 0, s, p);
+// The gradients hold three tensors and the next row's: one run a lane up to eight waves.
+// (16,384 rows of 4096 in bf16: 97 us with eight waves of one run, 105 with four of two;
+// 8192 rows of 8192 103 with eight of two, 107 with sixteen of one.)  Rows side by side in a
+// workgroup make it four waves at least.
+int grad_waves(int C) { return C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : C <= 8192 ? 8 : 16; }
+int grad_rows(int C) { return std::max(4 / grad_waves(C), 1); }
+// Workgroups: twelve waves or one workgroup for each of the 256 compute units.
+unsigned grad_blocks(int64_t T, int C) {
+    const int rows = grad_rows(C), waves = rows * grad_waves(C);
+    return (unsigned)std::min<int64_t>((T + rows - 1) / rows, 256 * std::max(12 / waves, 1));
 }
 
-unsigned grad_blocks(int64_t T) { return (unsigned)std::min<int64_t>(T, 512); }
+template <typename T, int WPR, int ROWS> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {
+    const dim3 grid(blocks), block(64 * WPR * ROWS);
+    if (p.C <= 512 * WPR) hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, 1, ROWS>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, 2, ROWS>), grid, block, 0, s, p);
+    trace("add_norm_backward_kernel<waves=%d, rows=%d> grid=(%u) block=%d", WPR, ROWS, blocks, 64 * WPR * ROWS);
+}
+template <typename T> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {
+    switch (grad_waves(p.C)) {
+    case 1: return launch_grad<T, 1, 4>(p, blocks, s);
+    case 2: return launch_grad<T, 2, 2>(p, blocks, s);
+    case 4: return launch_grad<T, 4, 1>(p, blocks, s);
+    case 8: return launch_grad<T, 8, 1>(p, blocks, s);
+    default: return launch_grad<T, 16, 1>(p, blocks, s);
+    }
+}
 
 }  // namespace
 
-size_t add_norm_backward_workspace_bytes(int64_t T, int C) { return (size_t)grad_blocks(T) * C * 4; }
+size_t add_norm_backward_workspace_bytes(int64_t T, int C) { return T > 0 ? (size_t)grad_blocks(T, C) * C * 4 : 0; }
 
 hipError_t launch_add_norm(const kda_add_norm_args *a, hipStream_t s) {
     NormParams p = {};
@@ -320,16 +399,15 @@ hipError_t launch_add_norm_backward(const kda_add_norm_backward_args *a, hipStre
     p.T = a->total_tokens; p.C = a->channels; p.eps = a->eps;
     p.dys = a->dy_stride; p.ss = a->s_stride; p.drs = a->dresidual_stride; p.dxs = a->dx_stride;
     p.part = a->dweight ? static_cast<float *>(a->workspace) : nullptr;
-    const unsigned blocks = grad_blocks(p.T);
+    const unsigned blocks = grad_blocks(p.T, p.C);
     if (p.T > 0) {
         a->dtype == KDA_BF16 ? launch_grad<__bf16>(p, blocks, s) : launch_grad<float>(p, blocks, s);
-        trace("add_norm_backward_kernel grid=(%u) block=256", blocks);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (a->dweight) {
-        hipLaunchKernelGGL(weight_grad_kernel, dim3((p.C + 31) / 32), dim3(256), 0, s, p.part, (int)blocks, p.C, a->dweight);
-        trace("weight_grad_kernel grid=(%d) block=256", (p.C + 31) / 32);
+        hipLaunchKernelGGL(weight_grad_kernel, dim3((p.C + 31) / 32), dim3(1024), 0, s, p.part, (int)blocks, p.C, a->dweight);
+        trace("weight_grad_kernel grid=(%d) block=1024", (p.C + 31) / 32);
     }
     return hipGetLastError();
 }

@@ -132,7 +132,7 @@ def test_add_norm_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     ({"total_tokens": -1}, INV), ({"channels": 4}, UNS), ({"channels": 16392}, UNS), ({"dtype": 2}, INV),
     ({"eps": -1.0}, INV), ({"dy": None}, INV), ({"s": None}, INV), ({"dx": None}, INV), ({"workspace": None}, INV),
-    ({"workspace_bytes": 8 * 256 * 4 - 1}, INV), ({"workspace": _addr(6) + 4}, INV), ({"dweight": _addr(5) + 4}, INV),
+    ({"workspace_bytes": 2 * 256 * 4 - 1}, INV), ({"workspace": _addr(6) + 4}, INV), ({"dweight": _addr(5) + 4}, INV),
     ({"weight": _addr(3) + 8}, INV), ({"dx": _addr(0) + 16}, INV), ({"dx": _addr(1), "dx_stride": 264}, INV),
     ({"dx": _addr(3)}, INV), ({"dweight": _addr(4)}, INV), ({"dweight": _addr(3)}, INV), ({"workspace": _addr(0)}, INV),
     ({"dy_stride": 248}, INV), ({"dresidual_stride": 257}, INV)])
@@ -160,7 +160,7 @@ def test_workspace_sizes(lib):
     assert lib.kda_gated_scan_workspace_size(None) == 0 and lib.kda_gated_scan_backward_workspace_size(None) == 0
     assert lib.kda_add_norm_backward_workspace_size(None) == 0
     assert lib.kda_add_norm_backward_workspace_size(ctypes.byref(_norm_grad(dweight=None))) == 0
-    assert lib.kda_add_norm_backward_workspace_size(ctypes.byref(_norm_grad())) == 8 * 256 * 4
+    assert lib.kda_add_norm_backward_workspace_size(ctypes.byref(_norm_grad())) == 2 * 256 * 4
 
 
 def test_null_arguments_and_nothing_to_do(lib):
