@@ -209,9 +209,9 @@ __global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(Grad
     __shared__ float meet[ROWS > 1 ? ROWS - 1 : 1][ROWS > 1 ? 512 * WPR * NC : 1];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64 % WPR, sub = threadIdx.x / (64 * WPR);
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    // (sixteen waves leave a lane 128 registers: there the weights are read again, and the
-    // residual's gradient when it is needed)
-    constexpr bool KEEP = WPR < 16;
+    // (sixteen waves leave a lane 128 registers: there the weights are read again, the
+    // residual's gradient when it is needed, and in fp32 no row ahead)
+    constexpr bool KEEP = WPR < 16, AHEAD = KEEP || sizeof(T) == 2;
     float dw[NC][8] = {}, w[KEEP ? NC : 1][8];
     Eight<T> ns[NC], ng[NC], nr[NC];
     bool on[NC];
@@ -233,10 +233,11 @@ __global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(Grad
         }
     };
     int64_t t = (int64_t)blockIdx.x * ROWS + sub;
-    load(t);
+    if (AHEAD) load(t);
     // every wave of a workgroup makes the same turns: barriers stand inside
     int buf = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < p.T; t0 += step, t += step, buf ^= 1) {
+        if (!AHEAD) load(t);
         Eight<T> s[NC], g[NC], r[NC];
         float ss = 0.f, dot = 0.f;
 #pragma unroll
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(Grad
             ss += on[i] ? a : 0.f;
             dot += on[i] ? b : 0.f;
         }
-        load(t + step);
+        if (AHEAD) load(t + step);
         ss = wave_sum(ss);
         dot = wave_sum(dot);
         if (WPR > 1) {
@@ -324,10 +325,12 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *part, in
     if (slice == 0 && c < C) *reinterpret_cast<f32x4 *>(dw + c) = sums[0][lane];
 }
 
-// Waves a row takes: so many that a lane holds at most two runs of eight channels.  16,384
-// rows of 4096 in bf16 with 8-bit groups: 87 us with four waves of two runs, 142 with one
-// of eight; 32,768 rows of 1024 42 with one wave of two runs, 48 with four of half a run.
-int waves_of(int C) { return C <= 1024 ? 1 : C <= 2048 ? 2 : C <= 4096 ? 4 : C <= 8192 ? 8 : 16; }
+// Waves a row takes: so many that a lane holds one run of eight channels, up to eight
+// waves, two above.  16,384 rows of 4096 in bf16 with 8-bit groups: 84 us with eight waves
+// of one run, 87 with four of two, 142 with one of eight; the gradients, which hold three
+// tensors and the next row's, 96, 105 and 158; 8192 rows of 8192, gradients, 103 with eight
+// waves of two runs, 107 with sixteen of one.
+int waves_of(int C) { return C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : C <= 8192 ? 8 : 16; }
 constexpr unsigned kMaxBlocks = 1u << 20;
 
 template <typename T, int QUANT, int WPR> void launch_norm(const NormParams &p, hipStream_t s) {
@@ -352,15 +355,12 @@ template <typename T> void launch_norm(const NormParams &p, int quant, hipStream
     else launch_norm<T, KDA_QUANT_GROUP>(p, s);
 }
 
-// The gradients hold three tensors and the next row's: one run a lane up to eight waves.
-// (16,384 rows of 4096 in bf16: 97 us with eight waves of one run, 105 with four of two;
-// 8192 rows of 8192 103 with eight of two, 107 with sixteen of one.)  Rows side by side in a
-// workgroup make it four waves at least.
-int grad_waves(int C) { return C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : C <= 8192 ? 8 : 16; }
-int grad_rows(int C) { return std::max(4 / grad_waves(C), 1); }
-// Workgroups: twelve waves or one workgroup for each of the 256 compute units.
+// Rows side by side in a workgroup of the gradients (four waves at least), and workgroups:
+// twelve waves or one workgroup for each of the 256 compute units (more of them add to the
+// partial sums of dweight: sixteen waves 104 us instead of 96).
+int grad_rows(int C) { return std::max(4 / waves_of(C), 1); }
 unsigned grad_blocks(int64_t T, int C) {
-    const int rows = grad_rows(C), waves = rows * grad_waves(C);
+    const int rows = grad_rows(C), waves = rows * waves_of(C);
     return (unsigned)std::min<int64_t>((T + rows - 1) / rows, 256 * std::max(12 / waves, 1));
 }
 
@@ -371,7 +371,7 @@ template <typename T, int WPR, int ROWS> void launch_grad(const GradParams &p, u
     trace("add_norm_backward_kernel<waves=%d, rows=%d> grid=(%u) block=%d", WPR, ROWS, blocks, 64 * WPR * ROWS);
 }
 template <typename T> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {
-    switch (grad_waves(p.C)) {
+    switch (waves_of(p.C)) {
     case 1: return launch_grad<T, 1, 4>(p, blocks, s);
     case 2: return launch_grad<T, 2, 2>(p, blocks, s);
     case 4: return launch_grad<T, 4, 1>(p, blocks, s);

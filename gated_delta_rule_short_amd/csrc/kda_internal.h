@@ -87,14 +87,14 @@ hipError_t launch_qk_norm_rope(const kda_qk_norm_rope_args *a, hipStream_t s);
 hipError_t launch_gated_norm(const kda_gated_norm_args *a, hipStream_t s);
 
 // Gated scan: `chained` with its tiles (numbered over all sequences) and workspace, or one
-// pass.  scan_tile: tokens of a tile; scan_chain_bytes: workspace of
+// pass.  scan_tile: tokens of a chained tile; scan_chain_bytes: workspace of
 // the chained schedule.
 struct ScanPlan {
     bool chained;
     int64_t tiles;
     void *workspace;
 };
-int scan_tile(kda_dtype dt, int gate, int input, bool backward, bool chained);
+int scan_tile(kda_dtype dt, int gate, int input, bool backward);
 size_t scan_chain_bytes(int64_t tiles, int C);
 hipError_t launch_gated_scan(const kda_gated_scan_args *a, const ScanPlan &plan, hipStream_t s);
 hipError_t launch_gated_scan_backward(const kda_gated_scan_backward_args *a, const ScanPlan &plan, hipStream_t s);

@@ -3,7 +3,7 @@
 //
 // The recurrence is linear in the state, so a run of tokens acts on the state before it
 // as one step (P, H): h -> P h + H, and runs are joined by (P2 P1, P2 H1 + H2).  A tile
-// is S tokens x 7 or 15 waves of 128 channels: a lane owns two neighbouring channels and a
+// is S tokens x 3, 7 or 15 waves of 128 channels: a lane owns two neighbouring channels and a
 // wave S tokens of them.  For each tile
 //   1. every wave forms its rows' step and leaves it in LDS;
 //   2. the manager, a wave of its own without rows, joins the steps, finds the state
@@ -108,11 +108,12 @@ template <typename T> __device__ __forceinline__ uint32_t lane_offset(const Scan
 // Rows whose factors are formed side by side: more would not fit the registers.
 constexpr int kTogether = 2;
 
-template <typename T, int GATE, int INPUT, bool CHAINED>
-__global__ void __launch_bounds__(64 * (scan_waves(CHAINED) + 1), scan_occupancy(sizeof(T), false, scan_cheap(GATE, INPUT))) scan_kernel(ScanParams p) {
+template <typename T, int GATE, int INPUT, int WAVES>
+__global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), false, scan_cheap(GATE, INPUT))) scan_kernel(ScanParams p) {
     typedef Two<T> two;
     constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), false, CHEAP);
-    constexpr int WAVES = scan_waves(CHAINED), S = scan_rows(sizeof(T), false, GATE, INPUT), TILE = S * WAVES;
+    constexpr bool CHAINED = WAVES == kWavesChained;
+    constexpr int S = scan_rows(sizeof(T), false, GATE, INPUT), TILE = S * WAVES;
     __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (wave == WAVES) {
@@ -196,11 +197,12 @@ __global__ void __launch_bounds__(64 * (scan_waves(CHAINED) + 1), scan_occupancy
 //     dh_t = do_t + r_t,  r_{t-1} = a_t dh_t,
 // as steps (P, H) of r -> P r + H with H = sum_t do_t a_first .. a_t.  The chain position
 // of a wave counts from the tile's end, that of a tile from the sequence's end.
-template <typename T, int GATE, int INPUT, bool CHAINED>
-__global__ void __launch_bounds__(64 * (scan_waves(CHAINED) + 1), scan_occupancy(sizeof(T), true, scan_cheap(GATE, INPUT))) scan_backward_kernel(ScanParams p) {
+template <typename T, int GATE, int INPUT, int WAVES>
+__global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), true, scan_cheap(GATE, INPUT))) scan_backward_kernel(ScanParams p) {
     typedef Two<T> two;
     constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), true, CHEAP);
-    constexpr int WAVES = scan_waves(CHAINED), S = scan_rows(sizeof(T), true, GATE, INPUT), TILE = S * WAVES;
+    constexpr bool CHAINED = WAVES == kWavesChained;
+    constexpr int S = scan_rows(sizeof(T), true, GATE, INPUT), TILE = S * WAVES;
     constexpr bool X = INPUT != KDA_INPUT_PLAIN;
     __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -310,24 +312,26 @@ __global__ void __launch_bounds__(256) scan_clear_kernel(uint4 *ws, int64_t word
     }
 }
 
-template <typename T, int GATE, int INPUT> void launch(const ScanParams &p, bool chained, bool backward, unsigned blocks, hipStream_t s) {
-    const dim3 grid(blocks), block(64 * (scan_waves(chained) + 1));
-    if (backward) {
-        if (chained) hipLaunchKernelGGL((scan_backward_kernel<T, GATE, INPUT, true>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((scan_backward_kernel<T, GATE, INPUT, false>), grid, block, 0, s, p);
-    } else {
-        if (chained) hipLaunchKernelGGL((scan_kernel<T, GATE, INPUT, true>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((scan_kernel<T, GATE, INPUT, false>), grid, block, 0, s, p);
-    }
+template <typename T, int GATE, int INPUT, int WAVES> void launch(const ScanParams &p, bool backward, unsigned blocks, hipStream_t s) {
+    const dim3 grid(blocks), block(64 * (WAVES + 1));
+    if (backward) hipLaunchKernelGGL((scan_backward_kernel<T, GATE, INPUT, WAVES>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((scan_kernel<T, GATE, INPUT, WAVES>), grid, block, 0, s, p);
 }
-template <typename T, int GATE> void launch(const ScanParams &p, int input, bool chained, bool backward, unsigned blocks, hipStream_t s) {
-    if (input == KDA_INPUT_PLAIN) launch<T, GATE, KDA_INPUT_PLAIN>(p, chained, backward, blocks, s);
-    else if (input == KDA_INPUT_COMPLEMENT) launch<T, GATE, KDA_INPUT_COMPLEMENT>(p, chained, backward, blocks, s);
-    else launch<T, GATE, KDA_INPUT_NORM>(p, chained, backward, blocks, s);
+template <typename T, int GATE, int INPUT> void launch(const ScanParams &p, int waves, bool backward, unsigned blocks, hipStream_t s) {
+    if (waves == kWavesChained) launch<T, GATE, INPUT, kWavesChained>(p, backward, blocks, s);
+    else if (waves == kWavesOnePass) launch<T, GATE, INPUT, kWavesOnePass>(p, backward, blocks, s);
+    else launch<T, GATE, INPUT, kWavesShort>(p, backward, blocks, s);
+}
+template <typename T, int GATE> void launch(const ScanParams &p, int input, int waves, bool backward, unsigned blocks, hipStream_t s) {
+    if (input == KDA_INPUT_PLAIN) launch<T, GATE, KDA_INPUT_PLAIN>(p, waves, backward, blocks, s);
+    else if (input == KDA_INPUT_COMPLEMENT) launch<T, GATE, KDA_INPUT_COMPLEMENT>(p, waves, backward, blocks, s);
+    else launch<T, GATE, KDA_INPUT_NORM>(p, waves, backward, blocks, s);
 }
 
 hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate, int input, bool backward, hipStream_t s) {
     unsigned blocks = (unsigned)((int64_t)p.N * p.groups);
+    const int rows = scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
+    const int waves = plan.chained ? kWavesChained : p.T <= (int64_t)p.N * kWavesShort * rows ? kWavesShort : kWavesOnePass;
     if (plan.chained) {
         p.tiles = (int)plan.tiles;
         char *ws = static_cast<char *>(plan.workspace);
@@ -343,18 +347,18 @@ hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (dt == KDA_BF16) gate == KDA_GATE_LOG ? launch<__bf16, KDA_GATE_LOG>(p, input, plan.chained, backward, blocks, s)
-                                             : launch<__bf16, KDA_GATE_SIGMOID>(p, input, plan.chained, backward, blocks, s);
-    else gate == KDA_GATE_LOG ? launch<float, KDA_GATE_LOG>(p, input, plan.chained, backward, blocks, s)
-                              : launch<float, KDA_GATE_SIGMOID>(p, input, plan.chained, backward, blocks, s);
-    trace("scan%s_kernel<%s> grid=(%u) block=%d", backward ? "_backward" : "", plan.chained ? "chained" : "one pass", blocks, 64 * (scan_waves(plan.chained) + 1));
+    if (dt == KDA_BF16) gate == KDA_GATE_LOG ? launch<__bf16, KDA_GATE_LOG>(p, input, waves, backward, blocks, s)
+                                             : launch<__bf16, KDA_GATE_SIGMOID>(p, input, waves, backward, blocks, s);
+    else gate == KDA_GATE_LOG ? launch<float, KDA_GATE_LOG>(p, input, waves, backward, blocks, s)
+                              : launch<float, KDA_GATE_SIGMOID>(p, input, waves, backward, blocks, s);
+    trace("scan%s_kernel<%s> grid=(%u) block=%d", backward ? "_backward" : "", plan.chained ? "chained" : "one pass", blocks, 64 * (waves + 1));
     return hipGetLastError();
 }
 
 }  // namespace
 
-int scan_tile(kda_dtype dt, int gate, int input, bool backward, bool chained) {
-    return scan_waves(chained) * scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
+int scan_tile(kda_dtype dt, int gate, int input, bool backward) {
+    return kWavesChained * scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
 }
 
 size_t scan_chain_bytes(int64_t tiles, int C) { return (size_t)ChainLayout(tiles, ((int64_t)C + 127) / 128).bytes; }

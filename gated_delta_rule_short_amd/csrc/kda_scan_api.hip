@@ -100,7 +100,7 @@ template <typename A> bool prefer_chained(const A &a, bool backward, int tile) {
 template <typename A> kda::ScanPlan scan_plan(const A &a, bool backward) {
     const kda::ScanPlan one{false, 0, nullptr};
     if (a.schedule == KDA_SCHEDULE_ONE_PASS || a.total_tokens < 1) return one;
-    const int tile = kda::scan_tile(a.dtype, a.gate_kind, a.input_kind, backward, true);
+    const int tile = kda::scan_tile(a.dtype, a.gate_kind, a.input_kind, backward);
     const kda::ScanPlan chained{true, a.total_tokens / tile + a.num_seqs, a.workspace};
     if (chained.tiles * channel_groups(a.channels) >= kMaxGroups) return one;
     return a.schedule == KDA_SCHEDULE_CHAINED || prefer_chained(a, backward, tile) ? chained : one;

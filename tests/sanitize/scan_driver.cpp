@@ -20,7 +20,7 @@ static kda::ScanPlan g_plan;
 static char g_msg[512];
 
 namespace kda {
-int scan_tile(kda_dtype dt, int, int, bool backward, bool chained) { return (chained ? 30 : 14) * (dt == KDA_F32 ? 1 : 2) * (backward ? 2 : 4); }
+int scan_tile(kda_dtype dt, int, int, bool backward) { return 30 * (dt == KDA_F32 ? 1 : 2) * (backward ? 2 : 4); }
 size_t scan_chain_bytes(int64_t tiles, int C) { return 256 + (size_t)((C + 127) / 128) * tiles * 1024; }
 hipError_t launch_gated_scan(const kda_gated_scan_args *a, const ScanPlan &p, hipStream_t) {
     ++g_launch; g_scan = *a; g_plan = p; return hipSuccess;
