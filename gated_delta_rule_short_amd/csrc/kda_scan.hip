@@ -105,8 +105,6 @@ template <typename T> __device__ __forceinline__ uint32_t lane_offset(const Scan
     return c < p.C ? (uint32_t)c * sizeof(T) : RowBuffer<T>::kNowhere;
 }
 
-// Rows whose factors are formed side by side: more would not fit the registers.
-constexpr int kTogether = 2;
 
 template <typename T, int GATE, int INPUT, int WAVES>
 __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), false, scan_cheap(GATE, INPUT))) scan_kernel(ScanParams p) {
@@ -163,7 +161,6 @@ __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), fa
                 const Factors<GATE, INPUT> f = factors(j, v);
                 run[v].before(f, u[j][v]);
             }
-            if (j % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
         sh.steps[wave][lane] = make_float4(run[0].log2_decay(), run[1].log2_decay(), run[0].add, run[1].add);
         barrier_lds();
@@ -187,7 +184,6 @@ __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), fa
             h.x = fmaf(a[j][0], h.x, u[j][0]);
             h.y = fmaf(a[j][1], h.y, u[j][1]);
             o.store(off, j, h.x, h.y);
-            if (AGAIN && (j + 1) % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
         cur = after;
     }
@@ -257,7 +253,6 @@ __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), tr
                 f[j][v] = Factors<GATE, INPUT>(two::get(rg[j], v));
                 run[v].behind(f[j][v], two::get(rd[j], v));
             }
-            if ((j + 1) % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
         sh.steps[pos][lane] = make_float4(run[0].log2_decay(), run[1].log2_decay(), run[0].add, run[1].add);
         barrier_lds();
@@ -287,7 +282,6 @@ __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), tr
             r = make_float2(m[0], m[1]);
             dx.store(off, j, ox[0], ox[1]);
             dg.store(off, j, og[0], og[1]);
-            if (AGAIN && j % kTogether == 0) __builtin_amdgcn_sched_barrier(0);
         }
         cur = after;
     }

@@ -16,6 +16,7 @@ using namespace kda::checks;
 
 // A launch holds fewer than 2^32 threads, up to 1024 of them in a workgroup.
 constexpr int64_t kMaxGroups = (int64_t)1 << 22;
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 512;
 
 int64_t channel_groups(int32_t C) { return ((int64_t)C + 127) / 128; }
 
@@ -45,8 +46,8 @@ kda_status check_strides(const Rows *r, int n) {
 template <typename A> kda_status check_tokens(const A &a) {
     const int64_t T = a.total_tokens;
     if (T < 0) return fail(KDA_ERR_INVALID_ARG, "total_tokens < 0");
-    // token positions inside a sequence are 32-bit in cu_seqlens
-    if (T > ((int64_t)1 << 31) - 64) return fail(KDA_ERR_INVALID_ARG, "total_tokens too large");
+    // token positions inside a sequence are 32-bit in the kernels, up to a tile past its end
+    if (T > kMaxTokens) return fail(KDA_ERR_INVALID_ARG, "total_tokens too large");
     if (a.cu_seqlens_host && !a.cu_seqlens) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens_host needs cu_seqlens");
     if (!a.cu_seqlens && T % a.num_seqs)
         return fail(KDA_ERR_INVALID_ARG, "cu_seqlens NULL needs total_tokens %% num_seqs == 0");
@@ -111,8 +112,7 @@ size_t plan_bytes(const kda::ScanPlan &plan, int32_t C) {
 }
 
 template <typename A> size_t scan_workspace(const A *a, bool backward) {
-    if (!a || a->num_seqs < 1 || a->channels < 1 || a->total_tokens < 0 || a->total_tokens > ((int64_t)1 << 31) - 64)
-        return 0;
+    if (!a || a->num_seqs < 1 || a->channels < 1 || a->total_tokens < 0 || a->total_tokens > kMaxTokens) return 0;
     return plan_bytes(scan_plan(*a, backward), a->channels);
 }
 

@@ -117,7 +117,9 @@ int kda_abi_version(void);
  * marks the workgroup, whose waves then wait no more: the call still ends, with
  * wrong results, instead of hanging.  The default (2^22 polls, restored by any
  * polls <= 0) is never reached by a correct hand-over.  Process-wide; takes
- * effect for launches after the call; returns the previous bound.
+ * effect for launches after the call; returns the previous bound.  The chained
+ * schedule of the gated scan is bounded by it too: there a tile that gives up on
+ * the state before it takes NaN for it.
  */
 int32_t kda_set_spin_limit(int32_t polls);
 
@@ -674,7 +676,7 @@ typedef enum { KDA_INPUT_PLAIN = 0, KDA_INPUT_COMPLEMENT = 1, KDA_INPUT_NORM = 2
 typedef struct {
     int32_t num_seqs;        /* N >= 1 */
     int32_t channels;        /* C: a positive multiple of 8 */
-    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 512 */
     kda_dtype dtype;
     kda_gate_kind gate_kind;
     kda_input_kind input_kind;
@@ -740,7 +742,7 @@ kda_status kda_gated_scan_decode(const kda_gated_scan_decode_args *args, hipStre
 typedef struct {
     int32_t num_seqs;        /* N >= 1 */
     int32_t channels;        /* C: a positive multiple of 8 */
-    int64_t total_tokens;    /* 0 <= T <= 2^31 - 64 */
+    int64_t total_tokens;    /* 0 <= T <= 2^31 - 512 */
     kda_dtype dtype;
     kda_gate_kind gate_kind;
     kda_input_kind input_kind;

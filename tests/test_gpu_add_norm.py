@@ -138,6 +138,21 @@ def test_add_norm_backward(T, C, dtype):
             assert dw is None
 
 
+def test_rows_past_one_launch_and_past_32_bits():
+    """More rows than one launch has workgroups, and more elements than 2^31, sampled."""
+    for T, C in ((1048576 + 77, 64), (280000, 8192)):
+        x = torch.randn(T, C, device=DEV, dtype=BF)
+        at = torch.tensor([0, 1, T // 2, T - 78, T - 2, T - 1], device=DEV)
+        y, scale, s = kda.kda_add_norm(x, x, quant="token")
+        rs, ref, bound = norm_ref(x[at], x[at], None, 1e-6)
+        check(s[at], rs, U16 * rs.abs(), "s")
+        check_quant(y[at], scale[at], ref, bound, "token")
+        dx, _ = kda.kda_add_norm_backward(x, s, dweight=False)
+        rx, _, ex, _ = norm_backward_ref(x[at], s[at], None, 1e-6, None)
+        check(dx[at], rx, U16 * rx.abs() + ex, "dx")
+        del x, y, s, dx
+
+
 def test_add_norm_backward_in_place_strided_and_empty():
     T, C = 40, 264
     wide = _rand((T, 3 * C + 16), 8, BF)

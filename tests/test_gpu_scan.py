@@ -385,6 +385,36 @@ def test_automatic_schedule_and_no_workspace():
     check_scan(*_prefill(inp, "log", "plain", cu_seqlens_host=[0, 300, 305]), inp, "log", "plain")
 
 
+def test_tensors_past_32_bits():
+    """More than 2^31 elements in each tensor, and tokens 2 MB apart over 10 GB: the last rows
+    against the recurrence over the tokens that still count."""
+    T, C = 270000, 8192
+    x = torch.randn(T, C, device=DEV, dtype=BF)
+    g = torch.full((T, C), -1.0, device=DEV, dtype=BF)
+    assert x.numel() > 1 << 31
+    for schedule in ("chained", "one_pass"):
+        o, state = kda.kda_gated_scan_prefill(x, g, state_out=True, schedule=schedule)
+        cols = torch.tensor([0, 5, 4097, 8191], device=DEV)
+        tail = {"x": x[-150:, cols], "gate": g[-150:, cols], "state": None, "slots": None, "lengths": [150]}
+        ro, rs, eo, es = scan_ref(tail, "log", "plain")  # e^-150 of what stands before
+        check(o[-40:, cols], ro[-40:], 2.0 ** -8 * ro[-40:].abs() + eo[-40:] + 1e-30, schedule + " o")
+        check(state[:, cols], rs, U32 * rs.abs() + es + 1e-30, schedule + " state")
+        dx, dg, _ = kda.kda_gated_scan_backward(x, g, o, schedule=schedule)
+        (rx, rg, _), (ex, eg, _) = backward_ref(tail, x[-150:, cols], o[-150:, cols], None, "log", "plain")
+        check(dx[-100:, cols], rx[-100:], 2.0 ** -8 * rx[-100:].abs() + ex[-100:] + 1e-30, schedule + " dx")
+        check(dg[-100:, cols], rg[-100:], 2.0 ** -8 * rg[-100:].abs() + eg[-100:] + 1e-30, schedule + " dgate")
+        del o, dx, dg
+    del x, g
+    wide = torch.empty(5000, 1 << 20, dtype=BF, device=DEV)
+    inp = make_scan([5000], 120, BF, "log", seed=17, device=DEV)
+    x, g, o = wide[:, :120], wide[:, 500000:500120], wide[:, 1000000:1000120]
+    x.copy_(inp["x"])
+    g.copy_(inp["gate"])
+    _, state = kda.kda_gated_scan_prefill(x, g, state_in=inp["state"], state_out=True, o=o)
+    want = kda.kda_gated_scan_prefill(inp["x"], inp["gate"], state_in=inp["state"], state_out=True)
+    assert torch.equal(o, want[0]) and torch.equal(state, want[1])
+
+
 def test_empty_batches():
     for dtype in (BF, F32):
         x = torch.empty(0, 16, dtype=dtype, device=DEV)

@@ -69,16 +69,18 @@ SHARED = [({"num_seqs": 0}, INV), ({"channels": 0}, INV), ({"channels": -8}, INV
           ({"flags": 1}, UNS), ({"flags": 256}, UNS), ({"num_seqs": 1 << 22}, INV), ({"gate": None}, INV),
           ({"o": None}, INV), ({"gate": _addr(1) + 8}, INV), ({"gate_stride": 71}, INV), ({"gate_stride": 76}, INV),
           ({"o_stride": -72}, INV), ({"gate_stride": 1 << 50}, INV)]
+WIDE = [({"gate_stride": (1 << 22) + 8}, UNS), ({"o_stride": (1 << 22) + 8}, UNS)]
 FORWARD = [({"x": None}, INV), ({"x": _addr(0) + 2}, INV), ({"x_stride": 64}, INV), ({"o": _addr(0)}, INV),
            ({"o": _addr(1) + 16}, INV), ({"state_slots": _addr(9)}, INV),
            ({"state_slots": _addr(9), "num_slots": -1}, INV), ({"state_slots": _addr(4), "num_slots": 4}, INV)]
-TOKENS = [({"total_tokens": -1}, INV), ({"total_tokens": 1 << 31}, INV), ({"total_tokens": 65, "cu_seqlens": None}, INV),
+TOKENS = [({"total_tokens": -1}, INV), ({"total_tokens": 1 << 31}, INV), ({"total_tokens": (1 << 31) - 511}, INV),
+          ({"total_tokens": 65, "cu_seqlens": None}, INV),
           ({"schedule": 2}, UNS), ({"schedule": 3}, UNS), ({"schedule": 5}, UNS), ({"schedule": -1}, UNS),
           ({"schedule": 4}, INV), ({"schedule": 4, "workspace": _addr(20), "workspace_bytes": 64}, INV),
           ({"schedule": 4, "workspace": _addr(20) + 8, "workspace_bytes": 1 << 20}, INV)]
 
 
-@pytest.mark.parametrize("kw,status", SHARED + FORWARD + TOKENS + [
+@pytest.mark.parametrize("kw,status", SHARED + WIDE + FORWARD + TOKENS + [
     ({"state_out": _addr(2) + 64}, INV), ({"state_out": _addr(0)}, INV), ({"state_in": _addr(2) + 4}, INV),
     ({"state_out": _addr(5)}, INV), ({"state_in": _addr(4)}, INV), ({"cu_seqlens": _addr(4)}, INV),
     ({"schedule": 4, "workspace": _addr(0), "workspace_bytes": 1 << 20}, INV),
@@ -95,7 +97,7 @@ def test_decode_refusals(lib, kw, status):
     assert lib.kda_last_error() != b""
 
 
-@pytest.mark.parametrize("kw,status", SHARED + TOKENS + [
+@pytest.mark.parametrize("kw,status", SHARED + WIDE + TOKENS + [
     ({"x": None}, INV), ({"input_kind": 0}, INV), ({"d_o": None}, INV), ({"dx": None}, INV), ({"dgate": None}, INV),
     ({"dx": _addr(0)}, INV), ({"dgate": _addr(6)}, INV), ({"dgate": _addr(1)}, INV), ({"dx": _addr(2)}, INV),
     ({"dx": _addr(3)}, INV), ({"dstate_in": _addr(6)}, INV), ({"dstate_in": _addr(4)}, INV),
@@ -150,11 +152,11 @@ def test_workspace_sizes(lib):
         assert size(backward, total_tokens=64) == 0                     # a tile: nothing to hand on
         assert size(backward, total_tokens=64, schedule=4) > 0          # asked for
         assert size(backward, total_tokens=1 << 16) > 0 and size(backward, total_tokens=1 << 16, schedule=1) == 0
-        for T in (1, 127, 128, 129, (1 << 31) - 64):                    # absurd calls stay arithmetic
+        for T in (1, 239, 240, 241, (1 << 31) - 512):                    # absurd calls stay arithmetic
             for C in (8, 1000, 2147483640):
                 size(backward, total_tokens=T, channels=C, schedule=4)
-    assert size(total_tokens=(1 << 31) - 64, schedule=4, channels=8) == 0   # too many tiles for a launch
-    a = _scan(cu_seqlens=None, num_seqs=1, total_tokens=(1 << 31) - 64, channels=8, schedule=4, workspace=1 << 60,
+    assert size(total_tokens=(1 << 31) - 512, schedule=4, channels=8) == 0  # too many tiles for a launch
+    a = _scan(cu_seqlens=None, num_seqs=1, total_tokens=(1 << 31) - 512, channels=8, schedule=4, workspace=1 << 60,
               workspace_bytes=1 << 60, x=_addr(1 << 10), gate=_addr(1 << 12), o=_addr(1 << 14))
     assert lib.kda_gated_scan_prefill(ctypes.byref(a), None) == INV and b"tiles" in lib.kda_last_error()
     assert lib.kda_gated_scan_workspace_size(None) == 0 and lib.kda_gated_scan_backward_workspace_size(None) == 0
