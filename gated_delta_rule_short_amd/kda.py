@@ -1104,11 +1104,13 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, y=None
 
 
 # ------------------------------------------------------------------ gated scan, norm with the residual
-_SCAN_PACK = struct.Struct("@2iq3iI3q8PiiPN")
+_SCAN_PACK = struct.Struct("@2iq3iI3q8Pii")            # and _WORKSPACE_PACK behind it
 _STEP_PACK = struct.Struct("@5iI3q5Pi4x")
-_SCAN_GRAD_PACK = struct.Struct("@2iq3iI6q11PiPN")
+_SCAN_GRAD_PACK = struct.Struct("@2iq3iI6q11Pi4x")     # likewise
 _ADD_NORM_PACK = struct.Struct("@q3if4q6P")
-_ADD_NORM_GRAD_PACK = struct.Struct("@qiif4q7PN")
+_ADD_NORM_GRAD_PACK = struct.Struct("@qiif4q6P")       # likewise
+_WORKSPACE_PACK = struct.Struct("@PN")
+_NO_WORKSPACE = _WORKSPACE_PACK.pack(0, 0)
 
 
 def _rows2(t, name, shape, dtype, dev):
@@ -1154,7 +1156,8 @@ def _cu(cu_seqlens, cu_seqlens_host, num_seqs, dev):
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         N = cu_seqlens.numel() - 1
-        _shape(cu_seqlens, "cu_seqlens", (N + 1,))
+        if cu_seqlens.dim() != 1:
+            _shape(cu_seqlens, "cu_seqlens", (N + 1,))
         cup = cu_seqlens.data_ptr()
     cuh = cu_seqlens_host
     if cuh is not None:
@@ -1236,28 +1239,26 @@ def kda_gated_scan_prefill(x, gate, *, gate_kind="log", input_kind="plain", cu_s
     if state_out is not None:
         sop = state_out.data_ptr()
 
-    def args(ws, size):
-        return _SCAN_PACK.pack(
-            N, C, T, code, gk, ik, flags, xs, gs, os_, x.data_ptr(), gate.data_ptr(), sip, sop, o.data_ptr(), cup,
-            0 if cuh is None else cuh.data_ptr(), slots, num_slots, sched, ws, size)
-
-    st = lib.kda_gated_scan_prefill(_with_workspace(lib.kda_gated_scan_workspace_size, args, workspace, dev),
-                                    _raw_stream(dev.index))
+    args, _ws = _with_workspace(
+        lib.kda_gated_scan_workspace_size,
+        _SCAN_PACK.pack(N, C, T, code, gk, ik, flags, xs, gs, os_, x.data_ptr(), gate.data_ptr(), sip, sop, o.data_ptr(),
+                        cup, 0 if cuh is None else cuh.data_ptr(), slots, num_slots, sched), workspace, dev)
+    st = lib.kda_gated_scan_prefill(args, _raw_stream(dev.index))
     if st:
         _check(lib, st)
     return o, state_out
 
 
 def _with_workspace(size_of, args, workspace, dev):
-    """Packed arguments with the workspace that the caller gave or that the call needs.
-    (An allocated one is freed on return: the allocator hands its memory on only to later
-    work of the same stream.)"""
+    """Packed arguments followed by the workspace that the caller gave or that the call
+    needs, and a reference to it.  (One made here is freed when the call returns: the allocator
+    hands its memory on only to later work of the same stream.)"""
     if workspace is True:
-        need = size_of(args(0, 0))
+        need = size_of(args + _NO_WORKSPACE)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if torch.is_tensor(workspace):
-        return args(workspace.data_ptr(), workspace.numel())
-    return args(0, 0)
+        return args + _WORKSPACE_PACK.pack(workspace.data_ptr(), workspace.numel()), workspace
+    return args + _NO_WORKSPACE, None
 
 
 def kda_gated_scan_decode(x, gate, state, *, gate_kind="log", input_kind="plain", o=None, state_slots=None, stream=None):
@@ -1352,15 +1353,14 @@ def kda_gated_scan_backward(d_o, gate, o, x=None, *, gate_kind="log", input_kind
     elif dstate_in is False:
         dstate_in = None
 
-    def args(ws, size):
-        return _SCAN_GRAD_PACK.pack(
+    args, _ws = _with_workspace(
+        lib.kda_gated_scan_backward_workspace_size,
+        _SCAN_GRAD_PACK.pack(
             N, C, T, code, gk, ik, flags, ds, gs, os_, xs, dxs, dgs, d_o.data_ptr(), gate.data_ptr(), o.data_ptr(), xp,
             0 if state_in is None else state_in.data_ptr(), 0 if dstate_out is None else dstate_out.data_ptr(),
             dx.data_ptr(), dgate.data_ptr(), 0 if dstate_in is None else dstate_in.data_ptr(), cup,
-            0 if cuh is None else cuh.data_ptr(), sched, ws, size)
-
-    st = lib.kda_gated_scan_backward(_with_workspace(lib.kda_gated_scan_backward_workspace_size, args, workspace, dev),
-                                     _raw_stream(dev.index))
+            0 if cuh is None else cuh.data_ptr(), sched), workspace, dev)
+    st = lib.kda_gated_scan_backward(args, _raw_stream(dev.index))
     if st:
         _check(lib, st)
     return dx, dgate, dstate_in
@@ -1467,12 +1467,11 @@ def kda_add_norm_backward(dy, s, weight=None, *, eps=1e-6, dresidual=None, dx=No
     elif dweight is False:
         dweight = None
 
-    def args(ws, size):
-        return _ADD_NORM_GRAD_PACK.pack(T, C, code, eps, ys, ss, rs, xs, dy.data_ptr(), s.data_ptr(), rp, wp,
-                                        dx.data_ptr(), 0 if dweight is None else dweight.data_ptr(), ws, size)
-
-    st = lib.kda_add_norm_backward(_with_workspace(lib.kda_add_norm_backward_workspace_size, args, workspace, dev),
-                                   _raw_stream(dev.index))
+    args, _ws = _with_workspace(
+        lib.kda_add_norm_backward_workspace_size,
+        _ADD_NORM_GRAD_PACK.pack(T, C, code, eps, ys, ss, rs, xs, dy.data_ptr(), s.data_ptr(), rp, wp, dx.data_ptr(),
+                                 0 if dweight is None else dweight.data_ptr()), workspace, dev)
+    st = lib.kda_add_norm_backward(args, _raw_stream(dev.index))
     if st:
         _check(lib, st)
     return dx, dweight

@@ -177,10 +177,11 @@ def test_null_arguments_and_nothing_to_do(lib):
 
 
 def test_struct_sizes():
-    for pack, s in ((K._SCAN_PACK, K.KdaGatedScanArgs), (K._STEP_PACK, K.KdaGatedScanDecodeArgs),
-                    (K._SCAN_GRAD_PACK, K.KdaGatedScanBackwardArgs), (K._ADD_NORM_PACK, K.KdaAddNormArgs),
-                    (K._ADD_NORM_GRAD_PACK, K.KdaAddNormBackwardArgs)):
-        assert pack.size == ctypes.sizeof(s)
+    for pack, s, ws in ((K._SCAN_PACK, K.KdaGatedScanArgs, True), (K._STEP_PACK, K.KdaGatedScanDecodeArgs, False),
+                        (K._SCAN_GRAD_PACK, K.KdaGatedScanBackwardArgs, True), (K._ADD_NORM_PACK, K.KdaAddNormArgs, False),
+                        (K._ADD_NORM_GRAD_PACK, K.KdaAddNormBackwardArgs, True)):
+        assert pack.size + (K._WORKSPACE_PACK.size if ws else 0) == ctypes.sizeof(s)
+        assert not ws or s.workspace.offset == pack.size
     assert K.KdaGatedScanArgs.x.offset == 56 and K.KdaGatedScanDecodeArgs.x.offset == 48
     assert K.KdaGatedScanBackwardArgs.d_o.offset == 80 and K.KdaAddNormArgs.x.offset == 56
     assert K.KdaAddNormBackwardArgs.dy.offset == 56
