@@ -88,6 +88,11 @@ struct NormParams {
     float eps;
 };
 
+// A workgroup takes one row (waves_of has the choice measured), eight or more stand on a
+// compute unit at a time and cover each other's sums.  The largest magnitude of a scale is
+// the largest of the bits, so that a NaN is above all others.  16,384 x 4096 bf16, 8-bit
+// groups: 472 MB in 84 to 87 us, 5.5 TB/s; one row of 4096 2.8 us.  A grid of workgroups that
+// stay was slower.
 template <typename T, int QUANT, int WPR, int NC>
 __global__ void __launch_bounds__(64 * WPR) add_norm_kernel(NormParams p) {
     __shared__ float part[2][WPR];
@@ -203,6 +208,8 @@ __device__ __forceinline__ void weights(const float *p, int at, float (&w)[8]) {
 // A workgroup of ROWS x WPR waves takes rows blockIdx x ROWS and on, a grid's rows apart,
 // with the next ones on their way while it works on these, and keeps the sums of dy n of
 // its channels in registers; its waves' sums meet in LDS at the end, one after another.
+// 16,384 x 4096 bf16: 541 MB in 94 us, 5.75 TB/s, and 5 for weight_grad_kernel; without the
+// next rows on their way 116 in all instead of 96.
 template <typename T, int WPR, int NC, int ROWS>
 __global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(GradParams p) {
     __shared__ float2 part[2][ROWS][WPR];
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(64 * WPR * ROWS) add_norm_backward_kernel(Grad
 }
 
 // dweight: 32 channels a workgroup, 8 lanes of four, 128 slices of the partial rows joined
-// through LDS in order.
+// through LDS in order (4.8 us for 256 rows of 4096: the launch and one trip to memory).
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *part, int rows, int C, float *dw) {
     __shared__ f32x4 sums[128][8];
     const int lane = threadIdx.x % 8, slice = threadIdx.x / 8, c = blockIdx.x * 32 + 4 * lane;
@@ -331,13 +338,15 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *part, in
 // tensors and the next row's, 96, 105 and 158; 8192 rows of 8192, gradients, 103 with eight
 // waves of two runs, 107 with sixteen of one.
 int waves_of(int C) { return C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : C <= 8192 ? 8 : 16; }
+// Of waves_of(C) waves, a lane holds one run (else two): only eight waves have both.
+template <int WPR> constexpr bool one_run(int C) { return WPR < 8 || (WPR == 8 && C <= 4096); }
 constexpr unsigned kMaxBlocks = 1u << 20;
 
 template <typename T, int QUANT, int WPR> void launch_norm(const NormParams &p, hipStream_t s) {
     const unsigned blocks = (unsigned)std::min<int64_t>(p.T, kMaxBlocks);
     const dim3 grid(blocks), block(64 * WPR);
-    if (p.C <= 512 * WPR) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 1>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, 2>), grid, block, 0, s, p);
+    if (one_run<WPR>(p.C)) hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, one_run<WPR>(1) ? 1 : 2>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((add_norm_kernel<T, QUANT, WPR, one_run<WPR>(1 << 30) ? 1 : 2>), grid, block, 0, s, p);
     trace("add_norm_kernel<waves=%d> grid=(%u) block=%d", WPR, blocks, 64 * WPR);
 }
 template <typename T, int QUANT> void launch_norm(const NormParams &p, hipStream_t s) {
@@ -366,8 +375,8 @@ unsigned grad_blocks(int64_t T, int C) {
 
 template <typename T, int WPR, int ROWS> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {
     const dim3 grid(blocks), block(64 * WPR * ROWS);
-    if (p.C <= 512 * WPR) hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, 1, ROWS>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, 2, ROWS>), grid, block, 0, s, p);
+    if (one_run<WPR>(p.C)) hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, one_run<WPR>(1) ? 1 : 2, ROWS>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((add_norm_backward_kernel<T, WPR, one_run<WPR>(1 << 30) ? 1 : 2, ROWS>), grid, block, 0, s, p);
     trace("add_norm_backward_kernel<waves=%d, rows=%d> grid=(%u) block=%d", WPR, ROWS, blocks, 64 * WPR * ROWS);
 }
 template <typename T> void launch_grad(const GradParams &p, unsigned blocks, hipStream_t s) {

@@ -8,22 +8,34 @@
 namespace kda {
 
 // A workgroup: waves with rows of a tile, one behind the other along the tokens, and
-// one that holds none and finds the tiles and their states.
-// Waves with rows: 15 where a sequence's tiles are chained (7: 1 x 65,536 tokens x 4096
-// 354 us instead of 337, 1 x 32,768 x 512 69 instead of 45: longer tiles make shorter
-// chains), 7 in one pass (15: 40 sequences of 0 to 90 tokens 26 us instead of 13.6), and 3
-// there where the sequences have no more tokens on average than they hold (7: 256 of 1 to
-// 60 tokens x 4096 channels 73 us instead of 47).
+// one that holds none and finds the tiles and their states.  Waves with rows: 15 where a
+// sequence's tiles are chained (7: 1 x 65,536 tokens x 4096 354 us instead of 337, 1 x 32,768
+// x 512 69 instead of 45: longer tiles make shorter chains), 7 in one pass (15: 40 sequences
+// of 0 to 90 tokens 26 us instead of 13.6), and 3 there where the sequences have no more
+// tokens on average than they hold (7: 256 of 1 to 60 tokens x 4096 channels 73 us instead
+// of 47).
 constexpr int kWavesChained = 15, kWavesOnePass = 7, kWavesShort = 3;
-// Factors that cost little are formed again in the second pass over the rows.
+
+// A wave goes over its rows twice.  Either it keeps two registers for every element from
+// one pass to the other, or it forms the factors again from the rows as they were read:
+// where they are cheap, so that 64 registers do and two workgroups of 16 waves fit a
+// compute unit (16 ragged sequences x 4096, log-decays 343 us, kept 372; pre-activations
+// with complement kept 337, formed again in 64 registers 977, most of it spills).  The
+// gradients of fp32, half as many rows to a wave, fit either way (8192 x 4096 160, kept 171).
 constexpr bool scan_cheap(int gate, int input) { return gate == KDA_GATE_LOG && input == KDA_INPUT_PLAIN; }
 constexpr bool scan_again(size_t elem, bool backward, bool cheap) { return cheap || (backward && elem == 4); }
 // Waves on a SIMD that the registers are cut for.
 constexpr int scan_occupancy(size_t elem, bool backward, bool cheap) { return elem == 4 || cheap ? 8 : 4; }
-// Tokens of a wave.
-constexpr int scan_rows(size_t elem, bool backward, int gate, int input) {
-    return backward ? 16 / (int)elem
-                    : elem == 2 ? (gate == KDA_GATE_SIGMOID && input == KDA_INPUT_NORM ? 14 : 16) : scan_cheap(gate, input) ? 8 : 6;
+// Tokens of a wave: what the registers hold (32,768 x 4096 bf16, pre-activations with norm:
+// 16 rows 227 us, 14 194; their gradients 10 rows 441, 8 345; gradients of log-decays with
+// complement 8 rows 328, 12 312, of pre-activations alone 8 289, 10 277, 12 298; 8192 x 4096
+// fp32 with norm 8 rows 92.6, 6 88.9), and no more where they all fit (log-decays alone
+// 16 rows, gradients 8 or 10 the same).  In one pass more rows leave waves without any (40
+// sequences of 40 tokens x 2048, gradients of log-decays with complement 8 rows 12.3, 12 14.4).
+constexpr int scan_rows(size_t elem, bool backward, bool chained, int gate, int input) {
+    const bool log = gate == KDA_GATE_LOG, plain = input == KDA_INPUT_PLAIN;
+    if (backward) return elem == 4 ? 4 : chained && log != plain ? (log ? 12 : 10) : 8;
+    return elem == 2 ? (!log && input == KDA_INPUT_NORM ? 14 : 16) : scan_cheap(gate, input) ? 8 : 6;
 }
 constexpr uint32_t kEmpty = 0xffffffffu, kState = 0xbf800000u;  // see chain_carry
 

@@ -7,17 +7,19 @@
 // wave S tokens of them.  For each tile
 //   1. every wave forms its rows' step and leaves it in LDS;
 //   2. the manager, a wave of its own without rows, joins the steps, finds the state
-//      before the tile and leaves each wave the state that it begins from.  Meanwhile the
-//      others send for the rows of the next tile, which the manager has found before;
+//      before the tile and leaves each wave the state that it begins from;
 //   3. every wave runs the recurrence over its rows and writes them.
-// Between tiles decays are handed on as logarithms, and only a whole tile's is rounded as
-// a decay: the rounding of every a = 1 - small, the same for every token of a steady
-// gate, would grow with the length of the memory.
+// Between waves and tiles decays are handed on as logarithms, and only a whole tile's is
+// rounded as a decay: the rounding of every a = 1 - small, the same for every token of a
+// steady gate, would grow with the length of the memory.
 //
 // One pass: a workgroup walks the tiles of one (sequence, 128 channels), the manager keeps
-// the state.  Chained: a workgroup takes tiles by ticket, and the state comes from the
+// the state.  Chained: a workgroup takes one tile by ticket, and the state comes from the
 // workgroup before it through the workspace (chain_carry).  Either way every element is
-// read once and written once: the bound is HBM.
+// read once and written once: the bound is HBM (figures at the kernels).  Workgroups that
+// stay and take tile after tile were slower, also with the next rows on their way (16 ragged
+// sequences of 75,926 tokens in all x 4096 channels 430 to 499 us, one tile each 391): a
+// ticket taken early waits for a tile that has not begun.
 #include <algorithm>
 
 #include "kda_scan.h"
@@ -105,13 +107,19 @@ template <typename T> __device__ __forceinline__ uint32_t lane_offset(const Scan
     return c < p.C ? (uint32_t)c * sizeof(T) : RowBuffer<T>::kNowhere;
 }
 
-
+// bf16, inputs not cached, bytes past L2: 1 x 4096 tokens x 8192 channels, log-decays, 208 MB
+// (1.03 of the least) in 51 us, 4.1 TB/s (1152 workgroups, 512 at a time: the ramps count);
+// 16 sequences of 75,926 tokens x 4096 343 us, 5.45 TB/s.  1 x 65,536 x 4096, pre-activations
+// with complement, 1.66 GB in 337 to 357 us, 4.7 to 4.9 TB/s: 126 registers leave a compute
+// unit one workgroup, and nothing is on its way while that one computes (VALU slots half
+// taken).  Half the rows in 64 registers, two workgroups: 354, and 179 instead of 184 for
+// 1 x 32,768 x 4096 log-decays with complement, 223 instead of 194 for pre-activations with norm.
 template <typename T, int GATE, int INPUT, int WAVES>
 __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), false, scan_cheap(GATE, INPUT))) scan_kernel(ScanParams p) {
     typedef Two<T> two;
     constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), false, CHEAP);
     constexpr bool CHAINED = WAVES == kWavesChained;
-    constexpr int S = scan_rows(sizeof(T), false, GATE, INPUT), TILE = S * WAVES;
+    constexpr int S = scan_rows(sizeof(T), false, CHAINED, GATE, INPUT), TILE = S * WAVES;
     __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (wave == WAVES) {
@@ -193,12 +201,14 @@ __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), fa
 //     dh_t = do_t + r_t,  r_{t-1} = a_t dh_t,
 // as steps (P, H) of r -> P r + H with H = sum_t do_t a_first .. a_t.  The chain position
 // of a wave counts from the tile's end, that of a tile from the sequence's end.
+// bf16: 1 x 4096 x 8192, log-decays, 349 MB in 76 us, 4.6 TB/s; 16 sequences of 92,117 tokens
+// x 4096, pre-activations with complement, 4.67 GB (1.03 of the least) in 884 us, 5.3 TB/s.
 template <typename T, int GATE, int INPUT, int WAVES>
 __global__ void __launch_bounds__(64 * (WAVES + 1), scan_occupancy(sizeof(T), true, scan_cheap(GATE, INPUT))) scan_backward_kernel(ScanParams p) {
     typedef Two<T> two;
     constexpr bool CHEAP = scan_cheap(GATE, INPUT), AGAIN = scan_again(sizeof(T), true, CHEAP);
     constexpr bool CHAINED = WAVES == kWavesChained;
-    constexpr int S = scan_rows(sizeof(T), true, GATE, INPUT), TILE = S * WAVES;
+    constexpr int S = scan_rows(sizeof(T), true, CHAINED, GATE, INPUT), TILE = S * WAVES;
     constexpr bool X = INPUT != KDA_INPUT_PLAIN;
     __shared__ Shared<WAVES> sh;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -298,7 +308,9 @@ struct ChainLayout {
     }
 };
 
-// Marks every word as not yet written, and sets flags and ticket to 0.
+// Marks every word as not yet written, and sets flags and ticket to 0: 5 to 7 us, most of
+// them the launch (26 MB for 1 x 65,536 x 4096).  A kernel and no fill of the runtime's,
+// which a captured graph does not replay reliably.
 __global__ void __launch_bounds__(256) scan_clear_kernel(uint4 *ws, int64_t words, int64_t end) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < end; i += (int64_t)gridDim.x * 256) {
         const uint32_t v = i < words ? 0u : kEmpty;
@@ -324,7 +336,7 @@ template <typename T, int GATE> void launch(const ScanParams &p, int input, int 
 
 hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate, int input, bool backward, hipStream_t s) {
     unsigned blocks = (unsigned)((int64_t)p.N * p.groups);
-    const int rows = scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
+    const int rows = scan_rows(dt == KDA_BF16 ? 2 : 4, backward, plan.chained, gate, input);
     const int waves = plan.chained ? kWavesChained : p.T <= (int64_t)p.N * kWavesShort * rows ? kWavesShort : kWavesOnePass;
     if (plan.chained) {
         p.tiles = (int)plan.tiles;
@@ -352,7 +364,7 @@ hipError_t launch_any(ScanParams p, const ScanPlan &plan, kda_dtype dt, int gate
 }  // namespace
 
 int scan_tile(kda_dtype dt, int gate, int input, bool backward) {
-    return kWavesChained * scan_rows(dt == KDA_BF16 ? 2 : 4, backward, gate, input);
+    return kWavesChained * scan_rows(dt == KDA_BF16 ? 2 : 4, backward, true, gate, input);
 }
 
 size_t scan_chain_bytes(int64_t tiles, int C) { return (size_t)ChainLayout(tiles, ((int64_t)C + 127) / 128).bytes; }

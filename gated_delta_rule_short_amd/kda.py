@@ -1152,7 +1152,7 @@ def _scan_schedule(schedule):
 
 def _cu(cu_seqlens, cu_seqlens_host, num_seqs, dev):
     """(N, device address, host tensor or None) of the sequences' bounds."""
-    N, cup = int(num_seqs or 1), 0
+    N, cup = 1 if num_seqs is None else int(num_seqs), 0
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         N = cu_seqlens.numel() - 1

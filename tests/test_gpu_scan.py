@@ -9,7 +9,7 @@ from tests._scan_common import (BF, DEV, F32, KINDS, U32, backward_ref, check, c
 
 pytestmark = pytest.mark.gpu
 SHAPES = [([1], 8), ([0, 1, 2], 120), ([15, 16, 17, 0], 128), ([127, 128, 129, 1], 136), ([300, 0, 700, 64], 264),
-          ([239, 240, 241, 480], 72)]
+          ([239, 240, 241, 480], 72), ([149, 150, 151, 179, 180, 181], 40)]
 
 
 @pytest.fixture(scope="module", autouse=True)

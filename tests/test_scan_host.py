@@ -205,6 +205,7 @@ def test_python_checks_scan_tensors():
             (dict(g=g.float()), TypeError, "gate must be"), (dict(x=x.t().contiguous().t()), ValueError, "dense"),
             (dict(x=x[:1].expand(6, 16)), ValueError, "overlap"), (dict(gate_kind="exp"), ValueError, "gate_kind"),
             (dict(input_kind="none"), ValueError, "input_kind"), (dict(schedule="two_pass"), ValueError, "schedule"),
+            (dict(state_in=st, num_seqs=0), ValueError, "state_in"),
             (dict(state_in=torch.zeros(2, 16)), ValueError, "state_in"), (dict(state_in=st.double()), TypeError, "state"),
             (dict(state_in=st, state_out=st.bfloat16()), TypeError, "one dtype"), (dict(o=x.float()), TypeError, "o must be"),
             (dict(cu_seqlens=torch.tensor([0, 6])), TypeError, "cu_seqlens"),
