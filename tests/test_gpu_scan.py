@@ -359,6 +359,48 @@ def test_captured_calls_replay():
         assert all(torch.equal(p, q) for p, q in zip(got, (w[0], w[1], b[0], b[1]))), i
 
 
+def test_captured_decode_advances_a_pool():
+    """Every replay is one more token of the sequences' slots, between eager steps of others."""
+    inp = make_scan([1] * 5, 264, BF, "log", BF, pool=9, seed=16, device=DEV)
+    x, pool, slots = inp["x"].clone(), inp["state"].clone(), inp["slots"]
+    o = torch.empty_like(x)
+    step = lambda p, out=None: kda.kda_gated_scan_decode(x, inp["gate"], p, input_kind="norm", o=out, state_slots=slots)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(pool.clone(), o)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(pool, o)
+    want = inp["state"].clone()
+    for i in range(4):
+        x.copy_(torch.randn(5, 264, generator=torch.Generator().manual_seed(i)).to(BF).to(DEV))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(step(want), o) and torch.equal(want, pool), i
+
+
+@pytest.mark.parametrize("count", [5, 70])
+@pytest.mark.parametrize("schedule", ["one_pass", "chained"])
+def test_states_of_a_pool_in_place(count, schedule):
+    """state_out is state_in: the first tile of a sequence reads the row that the last one
+    writes; rows of the pool that no sequence has stay."""
+    lengths = [(97 * i * i + 13 * i) % 700 for i in range(count)]
+    inp = make_scan(lengths, 136, F32, "sigmoid", pool=count + 6, seed=17, device=DEV)
+    pool = inp["state"].clone()
+    kw = dict(state_slots=inp["slots"], schedule=schedule)
+    o, out = _prefill(inp, "sigmoid", "complement", state_in=pool, state_out=pool, **kw)
+    assert out is pool
+    other = inp["state"].clone()
+    o2, _ = _prefill(inp, "sigmoid", "complement", state_out=other, **kw)
+    assert torch.equal(o, o2) and torch.equal(pool, other)
+    check_scan(o, pool[inp["slots"].long()], inp, "sigmoid", "complement")
+    rest = torch.ones(count + 6, dtype=torch.bool, device=DEV)
+    rest[inp["slots"].long()] = False
+    assert torch.equal(pool[rest], inp["state"][rest])
+
+
 def test_two_streams_at_once():
     """Calls that overlap on streams of their own, a workspace each."""
     a = make_scan([5000], 264, F32, "log", seed=14, device=DEV)
