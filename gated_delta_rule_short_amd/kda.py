@@ -1111,6 +1111,7 @@ _ADD_NORM_PACK = struct.Struct("@q3if4q6P")
 _ADD_NORM_GRAD_PACK = struct.Struct("@qiif4q6P")       # likewise
 _WORKSPACE_PACK = struct.Struct("@PN")
 _NO_WORKSPACE = _WORKSPACE_PACK.pack(0, 0)
+_strided = torch.empty_strided  # (0.3 to 0.8 us less than torch.empty)
 
 
 def _rows2(t, name, shape, dtype, dev):
@@ -1233,7 +1234,7 @@ def kda_gated_scan_prefill(x, gate, *, gate_kind="log", input_kind="plain", cu_s
     if o is None:
         o = torch.empty_like(x, memory_format=_dense)
     if state_out is True:
-        state_out = torch.empty((N, C), dtype=sdt, device=dev)
+        state_out = _strided((N, C), (C, 1), dtype=sdt, device=dev)
     elif state_out is False:
         state_out = None
     if state_out is not None:
@@ -1255,7 +1256,7 @@ def _with_workspace(size_of, args, workspace, dev):
     hands its memory on only to later work of the same stream.)"""
     if workspace is True:
         need = size_of(args + _NO_WORKSPACE)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = _strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
     if torch.is_tensor(workspace):
         return args + _WORKSPACE_PACK.pack(workspace.data_ptr(), workspace.numel()), workspace
     return args + _NO_WORKSPACE, None
@@ -1349,7 +1350,7 @@ def kda_gated_scan_backward(d_o, gate, o, x=None, *, gate_kind="log", input_kind
     if dgate is None:
         dgate = torch.empty_like(d_o, memory_format=_dense)
     if dstate_in is True:
-        dstate_in = torch.empty((N, C), dtype=torch.float32, device=dev)
+        dstate_in = _strided((N, C), (C, 1), dtype=torch.float32, device=dev)
     elif dstate_in is False:
         dstate_in = None
 
@@ -1417,7 +1418,7 @@ def kda_add_norm(x, residual=None, weight=None, *, eps=1e-6, quant="none", resid
     if y is None:
         y = torch.empty_like(x, dtype=ydt, memory_format=_dense)
     if scale is None and qk:
-        scale = torch.empty(sshape, dtype=torch.float32, device=dev)
+        scale = _strided(sshape, (1,) if qk == 1 else (C // 128, 1), dtype=torch.float32, device=dev)
     st = lib.kda_add_norm(
         _ADD_NORM_PACK.pack(T, C, code, qk, eps, xs, rs, ss, ys, x.data_ptr(), rp, wp,
                             0 if residual_out is None else residual_out.data_ptr(), y.data_ptr(),
@@ -1463,7 +1464,7 @@ def kda_add_norm_backward(dy, s, weight=None, *, eps=1e-6, dresidual=None, dx=No
     if dx is None:
         dx = torch.empty_like(dy, memory_format=_dense)
     if dweight is True:
-        dweight = torch.empty((C,), dtype=torch.float32, device=dev)
+        dweight = _strided((C,), (1,), dtype=torch.float32, device=dev)
     elif dweight is False:
         dweight = None
 
