@@ -45,3 +45,12 @@ def slack(gate, backward):
     """The bound above, relative to h."""
     tile = 28 if backward else 42
     return (3 * (1 / float(steady(gate)[2]) / tile + 1) + 160 + 8 * abs(GATES[gate])) * U32
+
+
+def step_slack(gate, steps, values):
+    """Of the mean over `values` states of h_n / (a^n h_0) - 1 after n single steps without an
+    input: 1 - a is off by at most 9 + 1.3 |z| units each step; the step's rounding, of states
+    with random digits, is as often up as down, at most half an ulp, and its root mean square
+    ulp / sqrt(12), 0.58 units: eight times that of the mean of n x values of them."""
+    c = float(steady(gate)[2])
+    return (steps * c * (9 + 1.3 * abs(GATES[gate])) + 8 * 0.58 * (steps / values) ** 0.5) * U32

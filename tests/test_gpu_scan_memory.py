@@ -1,12 +1,12 @@
-"""Long memories of the gated scan: steady gates over tens of thousands of tokens, forward and
-backward, within bounds that a rounded decay would break (shown on the
+"""Long memories of the gated scan: steady gates over tens of thousands of tokens, forward,
+backward and in single steps, within bounds that a rounded decay would break (shown on the
 CPU in test_scan_precision_host).  Bounds: _scan_memory."""
 import pytest
 import torch
 
 import gated_delta_rule_short_amd as kda
 from tests._scan_common import BF, DEV, F32, KINDS, check, half_step, make_scan
-from tests._scan_memory import GATES, TOKENS, filled, input_factor, slack, steady
+from tests._scan_memory import GATES, TOKENS, filled, input_factor, slack, steady, step_slack
 
 pytestmark = pytest.mark.gpu
 C = 136  # two groups of channels, the second not full
@@ -55,6 +55,20 @@ def test_steady_gates_backward(gate, inputs, dtype, schedule):
     want = dh * slope * (2.0 - q)
     check(dg[at], want, half_step(dtype) * want.abs() + tol * dh * slope * (2.0 + q), "dgate")
     check(ds, a * dh[:1], tol * a * dh[:1], "dstate_in")
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+def test_steady_gates_in_single_steps(gate):
+    """400 tokens without an input, states of random digits: the mean decay is the gate's own
+    and not that of its fp32 rounding, which would be off by 200 u32."""
+    steps, gen = 400, torch.Generator().manual_seed(1)
+    h = (1.0 + torch.rand(4, 8192, generator=gen)).to(DEV)
+    first = h.double()
+    x, g = torch.zeros(4, 8192, device=DEV), torch.full((4, 8192), GATES[gate], device=DEV)
+    for _ in range(steps):
+        kda.kda_gated_scan_decode(x, g, h, gate_kind=gate)
+    drift = float((h.double() / first).mean() * torch.exp(-steps * steady(gate)[0]) - 1.0)
+    assert abs(drift) <= step_slack(gate, steps, h.numel()), drift
 
 
 @pytest.mark.parametrize("gate,inputs", KINDS)
