@@ -7,8 +7,6 @@
 // round of them: half of it is the way to memory and back).  A channel
 // that remembers long is stepped as h - (1 - a) h: over thousands of calls the rounding
 // of a itself, the same at every step of a steady gate, would change its memory's length.
-#include <algorithm>
-
 #include "kda_scan.h"
 
 namespace kda {
@@ -19,7 +17,8 @@ struct StepParams {
     const void *x, *g;
     void *state, *o;
     const int32_t *slots;
-    int64_t xs, gs, os, items;  // items: sequences x C / 4
+    int64_t xs, gs, os;
+    unsigned items;  // sequences x C / 4: fewer than 2^27, since sequences x groups of 128 are fewer than 2^22
     int C, num_slots;
 };
 
@@ -34,24 +33,23 @@ __device__ __forceinline__ void store4(float *p, f32x4 v) { *reinterpret_cast<f3
 
 template <typename T, typename S, int GATE, int INPUT>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepParams p) {
-    const unsigned runs = p.C / 4;
-    for (int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x; item < p.items; item += (int64_t)gridDim.x * 256) {
-        const int n = (int)(item / runs), c = 4 * (int)(item - (int64_t)n * runs);
-        const int slot = pool_slot(p.slots, p.num_slots, n);
-        if (slot < 0) continue;
-        S *state = static_cast<S *>(p.state) + (size_t)slot * p.C + c;
-        const f32x4 x = load4(static_cast<const T *>(p.x) + n * p.xs + c), z = load4(static_cast<const T *>(p.g) + n * p.gs + c);
-        f32x4 h = load4(state);
+    const unsigned item = blockIdx.x * 256 + threadIdx.x, runs = p.C / 4;
+    if (item >= p.items) return;
+    const int n = (int)(item / runs), c = 4 * (int)(item - n * runs);
+    const int slot = pool_slot(p.slots, p.num_slots, n);
+    if (slot < 0) return;
+    S *state = static_cast<S *>(p.state) + (size_t)slot * p.C + c;
+    const f32x4 x = load4(static_cast<const T *>(p.x) + n * p.xs + c), z = load4(static_cast<const T *>(p.g) + n * p.gs + c);
+    f32x4 h = load4(state);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Factors<GATE, INPUT> f(z[i]);
-            const float u = f.input(x[i]), limited = __builtin_amdgcn_fmed3f(h[i], -3.4028234663852886e38f, 3.4028234663852886e38f);
-            // (an infinite state stays one: infinity minus a part of itself would not)
-            h[i] = f.c < 0.5f ? h[i] + fmaf(-f.c, limited, u) : fmaf(f.a, h[i], u);
-        }
-        store4(state, h);
-        store4(static_cast<T *>(p.o) + n * p.os + c, h);
+    for (int i = 0; i < 4; ++i) {
+        const Factors<GATE, INPUT> f(z[i]);
+        const float u = f.input(x[i]), limited = __builtin_amdgcn_fmed3f(h[i], -3.4028234663852886e38f, 3.4028234663852886e38f);
+        // (an infinite state stays one: infinity minus a part of itself would not)
+        h[i] = f.c < 0.5f ? h[i] + fmaf(-f.c, limited, u) : fmaf(f.a, h[i], u);
     }
+    store4(state, h);
+    store4(static_cast<T *>(p.o) + n * p.os + c, h);
 }
 
 template <typename T, typename S, int GATE> void launch(const StepParams &p, int input, unsigned blocks, hipStream_t s) {
@@ -70,8 +68,8 @@ hipError_t launch_gated_scan_decode(const kda_gated_scan_decode_args *a, hipStre
     p.x = a->x; p.g = a->gate; p.state = a->state; p.o = a->o;
     p.xs = a->x_stride; p.gs = a->gate_stride; p.os = a->o_stride;
     p.slots = a->state_slots; p.num_slots = a->num_slots; p.C = a->channels;
-    p.items = (int64_t)a->num_seqs * (a->channels / 4);
-    const unsigned blocks = (unsigned)std::min<int64_t>((p.items + 255) / 256, 1 << 22);
+    p.items = (unsigned)a->num_seqs * (unsigned)(a->channels / 4);
+    const unsigned blocks = (p.items + 255) / 256;
     const bool half = (a->flags & KDA_F_STATE_BF16) != 0;
     if (a->dtype == KDA_BF16) half ? launch<__bf16, __bf16>(p, a->gate_kind, a->input_kind, blocks, s) : launch<__bf16, float>(p, a->gate_kind, a->input_kind, blocks, s);
     else half ? launch<float, __bf16>(p, a->gate_kind, a->input_kind, blocks, s) : launch<float, float>(p, a->gate_kind, a->input_kind, blocks, s);
