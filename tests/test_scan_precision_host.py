@@ -1,5 +1,9 @@
 """The arithmetic of the gated scan's decays, evaluated on the CPU in fp32: what a rounded
-decay would cost on the gates of test_gpu_scan_memory, and that the bounds there see it."""
+decay would cost on the gates of test_gpu_scan_memory, and that the bounds there see it; and
+the errors that kda_scan.h states for its series and for the logistic function."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -43,3 +47,55 @@ def test_single_steps_by_the_complement(gate):
     off = [abs(float((v.astype(np.float64) / first).mean()) * np.exp(-steps * la) - 1.0) for v in (h, naive)]
     bound = step_slack(gate, steps, first.size)
     assert off[0] <= bound and off[1] > 30 * bound, [v / U32 for v in off + [bound]]
+
+
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gated_delta_rule_short_amd", "csrc",
+                      "kda_scan.h")
+
+
+def _body(head):
+    """The source of the device function whose declaration holds `head`."""
+    text = open(SOURCE, encoding="utf-8").read()
+    at = text.index(head)
+    return text[at:text.index("}\n", at)]
+
+
+def _worst(got, want):
+    return float((np.abs(got.astype(np.float64) - want) / np.abs(want)).max())
+
+
+def test_the_logarithm_of_1_plus_e():
+    """log2_1p over 2^-30 to 1, in fp32 as the source has it: 2.1e-7 of itself."""
+    body = _body("float log2_1p(float e)")
+    coeff = [f32(v) for v in re.findall(r"(-?\d\.\d+)f", body)]
+    assert len(coeff) == 9 and body.count("fmaf(") == 8
+    e = np.concatenate([np.exp2(np.linspace(-30, 0, 200001)), np.linspace(0.25, 1.0, 200001)]).astype(f32)
+    q = np.full_like(e, coeff[0])
+    for k in coeff[1:]:
+        q = _fma(q, e, k)
+    assert 1.5e-7 < _worst((e * q).astype(f32), np.log1p(e.astype(np.float64)) / np.log(2.0)) < 2.1e-7
+
+
+def test_1_minus_the_exponential_near_0():
+    """near_zero over -1/8 to -1e-8: 9e-8 of itself."""
+    body = _body("float near_zero(float g)")
+    assert [int(v) for v in re.findall(r"1\.f / (\d+)\.f", body)] == [720, 120, 24, 6] and body.count("fmaf(") == 5
+    g = -np.concatenate([np.exp2(np.linspace(-26, -3, 200001)), np.linspace(0.0625, 0.125, 200001)]).astype(f32)
+    q = _fma(g, f32(1.0) / f32(720.0), f32(1.0) / f32(120.0))
+    for k in (f32(1.0) / f32(24.0), f32(1.0) / f32(6.0), f32(0.5), f32(1.0)):
+        q = _fma(q, g, k)
+    assert 6e-8 < _worst((-g * q).astype(f32), -np.expm1(g.astype(np.float64))) < 9e-8
+
+
+def test_the_logistic_function_and_its_complement():
+    """a and 1 - a from one exponential, with every step rounded once: the argument's rounding
+    costs 1.3 |z| u32, four roundings the rest.  (The hardware's exponential and reciprocal may
+    be another u32 off, each.)"""
+    z = np.linspace(-60.0, 60.0, 400001).astype(f32)
+    e = np.exp2((-np.abs(z) * f32(1.4426950408889634)).astype(f32).astype(np.float64)).astype(f32)
+    r = (1.0 / (f32(1.0) + e).astype(f32).astype(np.float64)).astype(f32)
+    er = (e * r).astype(f32)
+    z64 = z.astype(np.float64)
+    for got, want in ((np.where(z > 0, r, er), 1.0 / (1.0 + np.exp(-z64))), (np.where(z > 0, er, r), 1.0 / (1.0 + np.exp(z64)))):
+        off = np.abs(got.astype(np.float64) - want) / want / U32
+        assert (off <= 4 + 1.3 * np.abs(z64)).all() and (off > 10).any()
