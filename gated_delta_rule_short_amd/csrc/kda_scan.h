@@ -26,12 +26,18 @@ constexpr bool scan_cheap(int gate, int input) { return gate == KDA_GATE_LOG && 
 constexpr bool scan_again(size_t elem, bool backward, bool cheap) { return cheap || (backward && elem == 4); }
 // Waves on a SIMD that the registers are cut for.
 constexpr int scan_occupancy(size_t elem, bool backward, bool cheap) { return elem == 4 || cheap ? 8 : 4; }
-// Tokens of a wave: what the registers hold (32,768 x 4096 bf16, pre-activations with norm:
-// 16 rows 227 us, 14 194; their gradients 10 rows 441, 8 345; gradients of log-decays with
-// complement 8 rows 328, 12 312, of pre-activations alone 8 289, 10 277, 12 298; 8192 x 4096
-// fp32 with norm 8 rows 92.6, 6 88.9), and no more where they all fit (log-decays alone
-// 16 rows, gradients 8 or 10 the same).  In one pass more rows leave waves without any (40
-// sequences of 40 tokens x 2048, gradients of log-decays with complement 8 rows 12.3, 12 14.4).
+// Tokens of a wave: about what the registers hold (32,768 x 4096 bf16, pre-activations with
+// norm: 16 rows 227 us, 14 194; their gradients 10 rows 441, 8 345; gradients of log-decays
+// with complement 8 rows 328, 12 312, of pre-activations alone 8 289, 10 277, 12 298; 8192 x
+// 4096 fp32 with norm 8 rows 92.6, 6 88.9).  Not to the last register: bf16 log-decays with
+// complement or norm take all 128 at 16 rows, and the forms of 7 and 3 waves keep 12 bytes a
+// lane in scratch (14 rows would take 121 and none); of the fp32 gradients log-decays with norm
+// at 7 and 3 waves and pre-activations alone at 15 keep 36.  Log-decays alone would hold more
+// than 16: 20 rows, 60 registers, are the same for wide prompts (1 x 4096 x 8192 51.4 us
+// either way, 16 ragged sequences x 4096 342 and 343) and better for long narrow ones (1 x
+// 32,768 x 512 40.4 instead of 44.7); their gradients are the same with 8 or 10.  In one pass
+// more rows leave waves without any (40 sequences of 40 tokens x 2048, gradients of log-decays
+// with complement 8 rows 12.3, 12 14.4).
 constexpr int scan_rows(size_t elem, bool backward, bool chained, int gate, int input) {
     const bool log = gate == KDA_GATE_LOG, plain = input == KDA_INPUT_PLAIN;
     if (backward) return elem == 4 ? 4 : chained && log != plain ? (log ? 12 : 10) : 8;

@@ -84,9 +84,11 @@ template <typename A> double padded_tokens(const A &a, int tile) {
 // time at 4.7 to 5.2 TB/s, of which a row that only pads a last tile costs half.  Measured,
 // one pass / chained, 4096 channels of bf16: 1 sequence of 224 tokens 10.5/14.0, 448
 // 16.6/14.5, 4096 137/35; 8 of 1000 47/52; 64 of 1000, log-decays 326/309, pre-activations
-// with complement 320/375; backward, 8 of 2000 142/137.  Lengths that only the device
-// knows count as one sequence: chained loses up to a third on many short ones, one pass
-// any factor on a long one among them.
+// with complement 320/375; backward, 8 of 2000 142/137.  Called one after another neither
+// side takes less than its fixed part, about 10 and 14, so the choice is early for one
+// sequence of a few hundred tokens: fp32, 224 x 512, takes chained, 14.4, and one pass would
+// take 10.7.  Lengths that only the device knows count as one sequence: chained loses up to
+// a third on many short ones, one pass any factor on a long one among them.
 template <typename A> bool prefer_chained(const A &a, bool backward, int tile) {
     const bool half = a.dtype == KDA_BF16, cheap = a.gate_kind == KDA_GATE_LOG && a.input_kind == KDA_INPUT_PLAIN;
     const double row = (double)a.channels * (half ? 2 : 4) * (!backward ? 3 : a.input_kind == KDA_INPUT_PLAIN ? 5 : 6);
