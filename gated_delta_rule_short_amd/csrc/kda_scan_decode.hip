@@ -2,11 +2,13 @@
 // h <- a h + b x, o = h, the states updated in place.
 //
 // A lane owns four neighbouring channels of one sequence.  The bound is HBM (every state
-// is read once and written once), or the launch where there are few sequences: 1 x 8192
-// channels 2.8 us, 256 x 8192 with slots 7.2 us for 29 MB, 4.1 TB/s (2048 workgroups, one
-// round of them: half of it is the way to memory and back).  A channel
-// that remembers long is stepped as h - (1 - a) h: over thousands of calls the rounding
-// of a itself, the same at every step of a steady gate, would change its memory's length.
+// is read once and written once) or, long before it, latency: 1 x 8192 channels 3.0 us, 256 x
+// 8192 with slots 7.1 us for 29 MB, 4.1 TB/s, in fp32 8.4 us for 42 MB, 5.0 TB/s.  2048
+// workgroups are one round of them, and with slots each makes two trips to memory, one behind
+// the other: the slot, which decides whether the sequence is there at all, then x, gate and
+// state.  A channel that remembers long is stepped as h - (1 - a) h: over thousands of calls
+// the rounding of a itself, the same at every step of a steady gate, would change its memory's
+// length.
 #include "kda_scan.h"
 
 namespace kda {
