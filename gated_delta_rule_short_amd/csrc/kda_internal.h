@@ -14,7 +14,8 @@ namespace kda {
 bool trace_on();
 void trace(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 
-// Polls of a fused-prefill hand-over wait before it gives up (kda_set_spin_limit).
+// Polls of a fused-prefill hand-over wait, or of a chained scan's tile, before it gives up
+// (kda_set_spin_limit).
 int spin_limit();
 
 // Conv over packed sequences; x, y: [T][channels].

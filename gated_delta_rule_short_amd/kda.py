@@ -374,10 +374,10 @@ def abi_version():
 
 
 def set_spin_limit(polls):
-    """Bound of the fused prefill's hand-over waits, for tests of its failure path
-    (kda_set_spin_limit): after `polls` unsuccessful polls a wait gives up and the
-    call ends with wrong results instead of hanging.  polls <= 0 restores the
-    default.  Returns the previous bound."""
+    """Bound of the waits of the fused prefill's hand-over and of the chained gated scan,
+    for tests of their failure paths (kda_set_spin_limit): after `polls` unsuccessful
+    polls a wait gives up and the call ends with wrong results (the scan's: NaN) instead
+    of hanging.  polls <= 0 restores the default.  Returns the previous bound."""
     return load_library().kda_set_spin_limit(int(polls))
 
 
@@ -1185,8 +1185,10 @@ def kda_gated_scan_prefill(x, gate, *, gate_kind="log", input_kind="plain", cu_s
     state_slots (int32 [N]) the state tensors are pools and sequence n uses row
     state_slots[n].  state_out: a tensor, or True to allocate one of state_in's dtype
     (else fp32).  schedule: "auto", "one_pass" or "chained" (include/kda.h).  workspace:
-    True allocates what the schedule needs, a uint8 tensor is used, None or False gives
-    none (one pass).  Returns (o, state_out)."""
+    True allocates what the schedule needs, a uint8 tensor is used (one that is too small
+    for the chosen schedule is an error), None or False gives none (one pass).  The outputs
+    carry no autograd history: kda_gated_scan_backward is called by the caller.  Returns
+    (o, state_out)."""
     lib = _lib or load_library()
     dev, dt = x.device, x.dtype
     if x.dim() != 2:
@@ -1306,7 +1308,9 @@ def kda_gated_scan_backward(d_o, gate, o, x=None, *, gate_kind="log", input_kind
     state_in are the forward call's (its output o holds the states); x too, which
     input_kind "plain" does not take.  dx, dgate: [T, C], allocated when not given;
     dstate_in: fp32 [N, C], or True to allocate it; it may be dstate_out.  In bf16 the
-    states are those that o holds, rounded once.  Returns (dx, dgate, dstate_in)."""
+    states are those that o holds, rounded once.  No autograd function calls it: the
+    gradients of what stands around the scan (conv, output norm, projections) are the
+    caller's.  Returns (dx, dgate, dstate_in)."""
     lib = _lib or load_library()
     dev, dt = d_o.device, d_o.dtype
     if d_o.dim() != 2:
@@ -1376,8 +1380,10 @@ def kda_add_norm(x, residual=None, weight=None, *, eps=1e-6, quant="none", resid
     of whole 16 bytes); weight fp32 [C] or None.  quant "none": y in x's dtype; "token" and
     "group": y / scale as float8_e4m3fn with fp32 scales [T], or [T, C / 128] (C a multiple
     of 128).  residual_out gets s in x's dtype: a tensor (x or residual in place), None to
-    allocate one where a residual is given, False for none.  Returns (y, scale, residual_out),
-    None where there is none."""
+    allocate one where a residual is given, False for none.  An 8-bit y is for the caller's
+    own products (kda_gate_beta_proj reads bf16).  The outputs carry no autograd history:
+    kda_add_norm_backward is called by the caller.  Returns (y, scale, residual_out), None
+    where there is none."""
     lib = _lib or load_library()
     dev, dt, shape = x.device, x.dtype, x.shape
     if x.dim() != 2:

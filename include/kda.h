@@ -666,9 +666,12 @@ kda_status kda_gated_norm(const kda_gated_norm_args *args, hipStream_t stream);
  * State [N][C], fp32 or bf16 with KDA_F_STATE_BF16; state_slots works as in "State pool"
  * above.  States, decays and 1 - a are formed and carried in fp32, decays as sums of
  * logarithms, and 1 - a without the cancellation: long memories keep their length.  o, and
- * a bf16 state, are rounded once.  A non-finite x, gate or state reaches later tokens of
+ * a bf16 state, are rounded once a call: a single step leaves a bf16 state as it is where it
+ * would move it by less than half a step, 2^-9 to 2^-8 of itself, so that channels with
+ * 1 - a below 2^-8 belong in fp32.  A non-finite x, gate or state reaches later tokens of
  * its own sequence and channel and nothing else; an infinity in a state may become NaN
- * once the decays behind it multiply to less than 2^-126.
+ * once the decays behind it multiply to less than 2^-126, where a finite state is taken to
+ * have gone.
  */
 typedef enum { KDA_GATE_LOG = 0, KDA_GATE_SIGMOID = 1 } kda_gate_kind;
 typedef enum { KDA_INPUT_PLAIN = 0, KDA_INPUT_COMPLEMENT = 1, KDA_INPUT_NORM = 2 } kda_input_kind;
@@ -705,8 +708,11 @@ typedef struct {
  *     it all the same, and a wait that gives up makes its outputs NaN.
  * KDA_SCHEDULE_AUTO takes the one expected to be faster where a workspace is given, by the
  * lengths that cu_seqlens_host (or equal sequences) shows; without them it takes the
- * batch for one long sequence.  The workspace is overwritten by each call and must not be
- * shared by calls that may overlap in time.  A token stride is at most 2^22 elements. */
+ * batch for one long sequence.  A workspace smaller than kda_gated_scan_workspace_size()
+ * returns KDA_ERR_INVALID_ARG where it would be used, under the automatic choice too: with
+ * KDA_SCHEDULE_ONE_PASS, or none, a call needs none.  The workspace is overwritten by each
+ * call and must not be shared by calls that may overlap in time.  A token stride is at most
+ * 2^22 elements. */
 kda_status kda_gated_scan_prefill(const kda_gated_scan_args *args, hipStream_t stream);
 
 /* Workspace bytes of the schedule that a call runs when it is given one (0: one pass).
@@ -738,7 +744,10 @@ kda_status kda_gated_scan_decode(const kda_gated_scan_decode_args *args, hipStre
  * with h_{t-1} read from the forward pass's o (and state_in before the first token): in
  * bf16 as it was rounded there.  A log-decay above 0 has no gradient; KDA_INPUT_NORM's
  * db/dz, infinite where a reaches 1, counts as 0 where b is 0.  dstate_out and dstate_in
- * are fp32.  States are not pooled here: sequence n owns row n. */
+ * are fp32.  States are not pooled here: sequence n owns row n.  A non-finite d_o, gate or
+ * dstate_out reaches its own token and earlier ones of its sequence and channel, x the
+ * gate's gradient of its own token, o that of the token behind it and state_in that of the
+ * first one; nothing else. */
 typedef struct {
     int32_t num_seqs;        /* N >= 1 */
     int32_t channels;        /* C: a positive multiple of 8 */

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_short_amd as kda
-from tests._scan_common import BF, DEV, F32, KINDS, check, half_step, make_scan
+from tests._scan_common import BF, DEV, F32, KINDS, U32, check, half_step, make_scan
 from tests._scan_memory import GATES, TOKENS, filled, input_factor, slack, steady, step_slack
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +85,17 @@ def test_long_chains_repeat(gate, inputs):
     o3, state3 = kda.kda_gated_scan_prefill(inp["x"][:9000], inp["gate"][:9000], state_in=inp["state"][:1].contiguous(),
                                             state_out=True, **kw)
     assert torch.equal(o3, o[:9000]) and torch.equal(state3, state[:1])
+
+
+def test_a_bf16_state_is_rounded_at_every_step():
+    """Steps of less than half a bf16 step leave the state, which the same steps in one
+    prompt, rounded once, move; steps of more than half a step move it."""
+    for gate, moves in ((-2.0 ** -10, False), (-2.0 ** -7, True)):
+        g, x = torch.full((64, 8), gate, device=DEV), torch.zeros(64, 8, device=DEV)
+        h = torch.ones(1, 8, dtype=BF, device=DEV)
+        for t in range(64):
+            kda.kda_gated_scan_decode(x[t:t + 1], g[t:t + 1], h)
+        assert (h != 1.0).all() if moves else (h == 1.0).all()
+        _, once = kda.kda_gated_scan_prefill(x, g, state_in=torch.ones(1, 8, dtype=BF, device=DEV), state_out=True)
+        want = torch.exp(torch.tensor(64.0 * gate, dtype=torch.float64)).expand(1, 8)
+        check(once, want, (half_step(BF) + 200 * U32) * want, "one prompt")

@@ -289,3 +289,18 @@ def test_host_code_under_address_and_undefined_sanitizers(tmp_path):
                            env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
         assert r.returncode == 0, "%s\n%s\n%s" % (" ".join(cmd), r.stdout[-4000:], r.stderr[-4000:])
     assert "scan sanitizer run ok" in r.stdout
+
+
+def test_a_workspace_too_small_is_refused_under_every_choice_that_uses_it(lib):
+    """The automatic choice takes no other schedule for a smaller workspace; one pass, and
+    calls that it is right for, need none."""
+    for make, size_of, call in (
+            (_scan, lib.kda_gated_scan_workspace_size, lib.kda_gated_scan_prefill),
+            (_grad, lib.kda_gated_scan_backward_workspace_size, lib.kda_gated_scan_backward)):
+        for sched in (0, 4):
+            args = dict(cu_seqlens=None, num_seqs=1, total_tokens=1 << 16, schedule=sched, workspace=_addr(20))
+            need = size_of(ctypes.byref(make(**args)))
+            assert need > 256
+            assert call(ctypes.byref(make(workspace_bytes=need - 1, **args)), None) == INV
+            assert b"needed" in lib.kda_last_error()
+        assert size_of(ctypes.byref(make(cu_seqlens=None, num_seqs=1, total_tokens=1 << 16, schedule=1))) == 0
