@@ -3,8 +3,8 @@
 
 With a gate value z at every token, a = 1 - c, and ones for x, the state from zero is
 h_t = b (1 - a^t) / c.  A rounding of a alone, by d, is a memory of another length: h is off
-by d / c of itself.  The gates here are the ones (of those that bf16 holds) whose a lies
-farthest from fp32: d is half a step, 2^-25, and d / c 1.2e-4 and 1.8e-4.
+by d / c of itself.  The gates here, which bf16 holds too, are ones whose a lies far from fp32:
+d is half a step, 2^-25, or nearly, and d / c 1.2e-4 and 1.7e-4.
 
 What the kernels may be off by, in units of u32 = 2^-24 of h (every term is positive):
   * 3 a tile: the exponential that makes the tile's decay (1 ulp, 2 units above 1/2) and the
